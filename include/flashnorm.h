@@ -307,6 +307,83 @@ FN_API fn_status flashnorm_linear_nvfp4(const void* x, const void* Q4, const voi
 FN_API fn_status flashnorm_nvfp4_workspace_bytes(int64_t M, int64_t d, int64_t N, int64_t* bytes);
 
 /*
+ * 8-bit integer projection (W8A8; the same Abstract item): weights with one scale per output channel, activations
+ * quantized on the fly with one scale per row, their product exact in int32. Prefill and decode sizes.
+ *     s[n]   = max_k |W*[n][k]| / 127  (1 for an all-zero channel),   W*[n][k] = g[k] W[k][n] (exact in fp32)
+ *     Q[n][k] = rint(W*[n][k] / s[n])   (the quotient in fp32, ties to even, within +-127)
+ *     a[m]   = max_k |x[m][k]|,   q[m][k] = rint(127 x[m][k] / a[m])  (the exact quotient, ties to even; 0 if a is 0)
+ *     rho[m] = a[m] / 127 / sqrt(mean_k x[m][k]^2 + eps)   (norm = 0: a[m] / 127)
+ *     y[m][n] = (sum_k q[m][k] Q[n][k]) rho[m] s[n],   GLU: silu(gate) * up of those values.
+ *   The deferred norm is free: 1/rms joins the row scale. A row with an infinity or a NaN is written as NaN.
+ * flashnorm_fold_weights_int8: W bf16 [d, N] row-major, g bf16 [d] -> Q int8 [N, d] K-major and scales fp32 [N]. glu as
+ *   for flashnorm_fold_weights (N = 2F; rows and their scales interleaved in blocks of FN_GLU_BLOCK).
+ * flashnorm_linear_int8: x bf16 [M, d] -> y [M, N] of out_dtype. norm = 0 leaves 1/rms out (a projection that no norm
+ *   precedes; fold with g = 1), eps is then ignored.
+ * flashnorm_glu_int8: Q and scales from the fold with glu = 1; y [M, F].
+ * flashnorm_int8_workspace_bytes: the scratch a call of this shape needs on the current device, written to *bytes
+ *   (codes, row scales, and for M <= FN_DECODE_MAX_M the partial sums of a split contraction). Caller-owned, 16-byte
+ *   aligned, contents irrelevant before and after; calls whose kernels may overlap on the GPU must not share one. A
+ *   smaller one returns FN_ERR_INVALID_ARG.
+ * Constraints: d % 16 == 0, 16 <= d <= 131072 (int32 sums), N % 8 == 0 (GLU: F % 16 == 0).
+ */
+FN_API fn_status flashnorm_fold_weights_int8(const void* W, const void* g, void* Q, void* scales, int64_t d, int64_t N,
+                                             int glu, void* stream);
+FN_API fn_status flashnorm_linear_int8(const void* x, const void* Q, const void* scales, void* y, int64_t M, int64_t d,
+                                       int64_t N, float eps, int norm, int out_dtype, void* workspace,
+                                       int64_t workspace_bytes, void* stream);
+FN_API fn_status flashnorm_glu_int8(const void* x, const void* Q, const void* scales, void* y, int64_t M, int64_t d,
+                                    int64_t F, float eps, int out_dtype, void* workspace, int64_t workspace_bytes,
+                                    void* stream);
+FN_API fn_status flashnorm_int8_workspace_bytes(int64_t M, int64_t d, int64_t N, int glu, int64_t* bytes);
+
+/* Which features of a head form a rotated pair: (2i, 2i + 1), or (i, i + rot_dim / 2). */
+typedef enum { FN_ROPE_INTERLEAVED = 0, FN_ROPE_HALF = 1 } fn_rope_layout;
+
+/* How a table stretches its angles for contexts longer than the trained one (flashnorm_rope_table_scaled). */
+typedef enum {
+  FN_ROPE_SCALE_NONE = 0,
+  FN_ROPE_SCALE_LINEAR = 1,
+  FN_ROPE_SCALE_NTK = 2,
+  FN_ROPE_SCALE_YARN = 3
+} fn_rope_scaling;
+
+/*
+ * flashnorm_rope — rotary positions on heads already in memory (the post-norm entry point below rotates in its own
+ * epilogue; this one serves projections without a per-head norm, the half layout, a rotated part of the head, and
+ * the gradient). For every row m, head h < n_rope_heads and pair i < rot_dim / 2, with (c, s) of table row
+ * positions[m]:
+ *     y[a] = x[a] c - x[b] s,   y[b] = x[a] s + x[b] c,     (a, b) = (2i, 2i+1) or (i, i + rot_dim/2),
+ * in fp32, rounded once. Features from rot_dim on and heads from n_rope_heads on are carried over bit for bit.
+ *   x, y       [M, H, head_dim] of dtype (FN_BF16 or FN_F32), head_dim contiguous, row and head strides in elements;
+ *              aligned to their elements (16-byte aligned bases and strides use wide accesses). y == x with equal
+ *              strides rotates in place; any other overlap is not allowed.
+ *   rope_cs    fp32 [max_pos][rot_dim / 2][2]; positions int32 [M], device memory. A position outside [0, max_pos)
+ *              writes the row's rotated features as NaN and the next flashnorm_check_device_error returns
+ *              FN_ERR_INVALID_ARG.
+ *   backward   1: the transposed rotation (s -> -s), which maps dL/dy to dL/dx.
+ * Constraints: rot_dim even, 2 <= rot_dim <= head_dim, 0 <= n_rope_heads <= H.
+ */
+FN_API fn_status flashnorm_rope(const void* x, const void* rope_cs, const void* positions, void* y, int64_t M, int64_t H,
+                                int64_t head_dim, int64_t rot_dim, int64_t n_rope_heads, int64_t max_pos,
+                                int64_t x_row_stride, int64_t x_head_stride, int64_t y_row_stride,
+                                int64_t y_head_stride, int layout, int backward, int dtype, void* stream);
+
+/*
+ * flashnorm_rope_table_scaled — a (cos, sin) table as flashnorm_rope_table's, for rot_dim features, with the angles
+ * of pair i, theta_i = base^(-2i / rot_dim), stretched for long contexts:
+ *   NONE    theta_i
+ *   LINEAR  theta_i / factor
+ *   NTK     base replaced by base * factor^(rot_dim / (rot_dim - 2))
+ *   YARN    theta_i (k_i + (1 - k_i) / factor), k_i = clamp((t_i - alpha) / (beta - alpha), 0, 1),
+ *           t_i = original_max_pos theta_i / (2 pi) ("YaRN: Efficient Context Window Extension of Large Language
+ *           Models", NTK-by-parts)
+ * cos and sin are both multiplied by attention_factor (1 for none). Double precision, rounded once to fp32.
+ */
+FN_API fn_status flashnorm_rope_table_scaled(void* rope_cs, int64_t max_pos, int64_t rot_dim, double base, int scaling,
+                                             double factor, double original_max_pos, double alpha, double beta,
+                                             double attention_factor, void* stream);
+
+/*
  * flashnorm_rope_table — fills rope_cs (fp32 [max_pos][head_dim / 2][2], caller-owned device memory,
  * 16-byte aligned) with cos and sin of p * base^(-2i/head_dim), computed in double precision and
  * rounded once to fp32. head_dim even, max_pos >= 1, base > 1 (RoFormer uses 10000). Asynchronous on

@@ -17,6 +17,7 @@ importing works but every call raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -40,6 +41,12 @@ __all__ = [
     "flashnorm_fold_weights_nvfp4",
     "flashnorm_linear_nvfp4",
     "flashnorm_nvfp4_workspace_bytes",
+    "flashnorm_fold_weights_int8",
+    "flashnorm_linear_int8",
+    "flashnorm_glu_int8",
+    "flashnorm_int8_workspace_bytes",
+    "flashnorm_rope",
+    "flashnorm_rope_table_scaled",
     "flashnorm_layernorm_linear",
     "flashnorm_rmsnorm",
     "flashnorm_linear_unfused",
@@ -65,6 +72,7 @@ PATHS = {"auto": 0, "tensor": 1, "gemv": 2, "decode": 3, "pair": 4}
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _F = ctypes.c_float
+_D = ctypes.c_double
 _INT = ctypes.c_int
 
 # name -> argtypes; restype is fn_status (int) unless listed in _RESTYPES
@@ -88,6 +96,12 @@ _SIGNATURES = {
     "flashnorm_fold_weights_nvfp4": [_P, _P, _P, _P, _I64, _I64, _P],
     "flashnorm_linear_nvfp4": [_P, _P, _P, _P, _I64, _I64, _I64, _F, _INT, _P, _I64, _P],
     "flashnorm_nvfp4_workspace_bytes": [_I64, _I64, _I64, _P],
+    "flashnorm_fold_weights_int8": [_P, _P, _P, _P, _I64, _I64, _INT, _P],
+    "flashnorm_linear_int8": [_P, _P, _P, _P, _I64, _I64, _I64, _F, _INT, _INT, _P, _I64, _P],
+    "flashnorm_glu_int8": [_P, _P, _P, _P, _I64, _I64, _I64, _F, _INT, _P, _I64, _P],
+    "flashnorm_int8_workspace_bytes": [_I64, _I64, _I64, _INT, _P],
+    "flashnorm_rope": [_P, _P, _P, _P] + [_I64] * 10 + [_INT, _INT, _INT, _P],
+    "flashnorm_rope_table_scaled": [_P, _I64, _I64, _D, _INT, _D, _D, _D, _D, _D, _P],
     "flashnorm_layernorm_linear": [_P, _P, _P, _P, _P, _I64, _I64, _I64, _F, _INT, _P],
     "flashnorm_rmsnorm": [_P, _P, _P, _I64, _I64, _F, _P],
     "flashnorm_linear_unfused": [_P, _P, _P, _P, _P, _I64, _I64, _I64, _F, _INT, _P],
@@ -605,6 +619,175 @@ def flashnorm_linear_postnorm_rope(x: torch.Tensor, Wstar: torch.Tensor, g2: tor
     _invoke("flashnorm_linear_postnorm_rope", x, _ptr(x), _ptr(Wstar), _ptr(g2), _ptr(rope_cs), _ptr(positions),
             _ptr(y), M, d, N, int(head_dim), int(n_rope_heads), int(rope_cs.shape[0]), float(eps2),
             _out_code(out_dtype), _stream_ptr(x))
+    return y
+
+
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def flashnorm_rope(x: torch.Tensor, rope_cs: torch.Tensor, positions: torch.Tensor, n_rope_heads=None,
+                   layout: str = "interleaved", backward: bool = False, out=None) -> torch.Tensor:
+    """Rotary positions on x [M, H, head_dim] (bf16 or fp32; any row and head strides, features contiguous).
+
+    rope_cs: fp32 [max_pos, rot_dim / 2, 2]; the first rot_dim features of the first n_rope_heads heads (default:
+    all) are turned by the angles of table row positions[m] (int32 [M]), the rest is carried over. layout: pairs
+    (2i, 2i+1), "interleaved", or (i, i + rot_dim/2), "half". backward=True applies the transposed rotation, which
+    maps the gradient of y to that of x. out=x rotates in place; other overlaps of out and x are not allowed."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
+    if x.dim() != 3:
+        raise ValueError(f"x must be [M, H, head_dim], got shape {tuple(x.shape)}")
+    _need(rope_cs, "rope_cs", torch.float32, dim=3)
+    _need(positions, "positions", torch.int32, dim=1)
+    M, H, hd = x.shape
+    max_pos, half, two = rope_cs.shape
+    if two != 2:
+        raise ValueError("rope_cs must be [max_pos, rot_dim / 2, 2]")
+    if positions.shape[0] != M:
+        raise ValueError("positions must have one entry per row of x")
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError('layout must be "interleaved" or "half"')
+    if x.stride(2) != 1 and hd > 1:
+        raise ValueError("the features of a head must be contiguous")
+    if out is None:
+        out = torch.empty((M, H, hd), dtype=x.dtype, device=x.device)
+    elif out is not x:
+        if not isinstance(out, torch.Tensor) or out.dtype != x.dtype:
+            raise TypeError(f"out must be a {x.dtype} tensor")
+        if out.shape != x.shape or (out.stride(2) != 1 and hd > 1):
+            raise ValueError("out must have the shape of x, with contiguous features")
+    _same_device(x, rope_cs=rope_cs, positions=positions, out=out)
+    _invoke("flashnorm_rope", x, _ptr(x), _ptr(rope_cs), _ptr(positions), _ptr(out), M, H, hd, 2 * half,
+            H if n_rope_heads is None else int(n_rope_heads), max_pos, x.stride(0), x.stride(1), out.stride(0),
+            out.stride(1), ROPE_LAYOUTS[layout], int(bool(backward)), FN_BF16 if x.dtype == torch.bfloat16 else FN_F32,
+            _stream_ptr(x))
+    return out
+
+
+def flashnorm_rope_table_scaled(max_pos: int, rot_dim: int, base: float = 10000.0, scaling: str = "none",
+                                factor: float = 1.0, original_max_pos=None, alpha: float = 1.0, beta: float = 32.0,
+                                attention_factor=None, device=None, out=None) -> torch.Tensor:
+    """(cos, sin) fp32 [max_pos, rot_dim / 2, 2] of rotary angles scaled for a context `factor` times the trained one.
+
+    scaling: "none"; "linear" (positions divided by factor); "ntk" (base times factor^(rot_dim / (rot_dim - 2)));
+    "yarn" (by parts: pairs that turn at least beta times within original_max_pos keep their angle, those that turn
+    at most alpha times are divided by factor, a linear blend between). attention_factor multiplies cos and sin;
+    the default is 0.1 ln(factor) + 1 for "yarn" and 1 otherwise."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError('scaling must be "none", "linear", "ntk" or "yarn"')
+    if scaling == "yarn" and original_max_pos is None:
+        raise ValueError('scaling="yarn" needs original_max_pos')
+    if attention_factor is None:
+        attention_factor = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" and factor > 0 else 1.0
+    max_pos, rot_dim = int(max_pos), int(rot_dim)
+    if max_pos < 1 or rot_dim < 2 or rot_dim % 2:
+        raise ValueError("max_pos must be positive, rot_dim positive and even")
+    if out is None:
+        dev = torch.device("cuda", torch.cuda.current_device() if device is None else device)
+        out = torch.empty(max_pos, rot_dim // 2, 2, dtype=torch.float32, device=dev)
+    else:
+        _need(out, "out", torch.float32)
+        if tuple(out.shape) != (max_pos, rot_dim // 2, 2):
+            raise ValueError("out must be [max_pos, rot_dim / 2, 2]")
+    _invoke("flashnorm_rope_table_scaled", out, _ptr(out), max_pos, rot_dim, float(base), ROPE_SCALINGS[scaling],
+            float(factor), float(original_max_pos or 0.0), float(alpha), float(beta), float(attention_factor),
+            _stream_ptr(out))
+    return out
+
+
+def flashnorm_fold_weights_int8(W: torch.Tensor, g: torch.Tensor, glu: bool = False):
+    """(Q int8 [N, d], scales fp32 [N]): the gain fold, then 8-bit integer quantization per output channel (GLU:
+    rows and scales with gate and up interleaved in blocks of 16)."""
+    _need(W, "W", dim=2)
+    _need(g, "g", dim=1)
+    d, N = W.shape
+    if g.shape[0] != d:
+        raise ValueError("g must have d elements")
+    _same_device(W, g=g)
+    Q = torch.empty(N, d, dtype=torch.int8, device=W.device)
+    scales = torch.empty(N, dtype=torch.float32, device=W.device)
+    _invoke("flashnorm_fold_weights_int8", W, _ptr(W), _ptr(g), _ptr(Q), _ptr(scales), d, N, int(bool(glu)),
+            _stream_ptr(W))
+    return Q, scales
+
+
+_int8_ws_bytes_cache = {}
+
+
+def flashnorm_int8_workspace_bytes(M: int, d: int, N: int, glu: bool = False, device=None) -> int:
+    """Workspace bytes flashnorm_linear_int8 (glu: flashnorm_glu_int8, with N = F) needs for this shape on `device`."""
+    dev = torch.cuda.current_device() if device is None else torch.device(device).index
+    if dev is None:
+        dev = torch.cuda.current_device()
+    key = (dev, M, d, N, glu)
+    hit = _int8_ws_bytes_cache.get(key)
+    if hit is not None:
+        return hit
+    nbytes = ctypes.c_int64(0)
+    _invoke_on(dev, "flashnorm_int8_workspace_bytes", int(M), int(d), int(N), int(bool(glu)), ctypes.addressof(nbytes))
+    if len(_int8_ws_bytes_cache) >= 4096:  # a server's ragged batches need not be remembered for ever
+        _int8_ws_bytes_cache.clear()
+    _int8_ws_bytes_cache[key] = int(nbytes.value)  # a function of the shape and the device's SM count only
+    return int(nbytes.value)
+
+
+def _call_workspace(workspace, nbytes: int, x: torch.Tensor):
+    """The scratch of one call: a fresh buffer ("auto": torch's allocator hands it on in stream order, and a captured
+    call's comes from its graph's pool, so no two calls that may overlap share one), or the caller's."""
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError('workspace must be "auto" or a uint8 CUDA tensor')
+        return torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    _need(workspace, "workspace", torch.uint8, dim=1)
+    _same_device(x, workspace=workspace)
+    return workspace
+
+
+def _int8_call(x, Q, scales, glu):
+    _need(x, "x", dim=2)
+    _need(Q, "Q", torch.int8, dim=2)
+    _need(scales, "scales", torch.float32, dim=1)
+    M, d = x.shape
+    rows = Q.shape[0]
+    if Q.shape[1] != d or scales.shape[0] != rows or (glu and rows % 2):
+        raise ValueError("Q [2F, d] and scales [2F] must match x [M, d]" if glu else
+                         "Q [N, d] and scales [N] must match x [M, d]")
+    _same_device(x, Q=Q, scales=scales)
+    return M, d, rows // 2 if glu else rows
+
+
+def flashnorm_linear_int8(x: torch.Tensor, Q: torch.Tensor, scales: torch.Tensor, eps: float,
+                          out_dtype=torch.bfloat16, out=None, norm: bool = True, workspace="auto") -> torch.Tensor:
+    """y = (q . Q^T) * rho * scales: x [M, d] bf16 quantized to 8-bit integers row by row, Q int8 [N, d] and scales from
+    flashnorm_fold_weights_int8, the product exact in int32, rho the row's scale times 1/rms (norm=False: without
+    1/rms, for a projection that no norm precedes). workspace: "auto", or a uint8 CUDA tensor of at least
+    flashnorm_int8_workspace_bytes(M, d, N) bytes."""
+    M, d, N = _int8_call(x, Q, scales, False)
+    y = _output(out, (M, N), out_dtype, x)
+    if M == 0:
+        return y
+    ws = _call_workspace(workspace, flashnorm_int8_workspace_bytes(M, d, N, False, x.get_device()), x)
+    _invoke("flashnorm_linear_int8", x, _ptr(x), _ptr(Q), _ptr(scales), _ptr(y), M, d, N, float(eps), int(bool(norm)),
+            _out_code(out_dtype), _ptr(ws), ws.numel(), _stream_ptr(x))
+    return y
+
+
+def flashnorm_glu_int8(x: torch.Tensor, Q_gu: torch.Tensor, scales: torch.Tensor, eps: float,
+                       out_dtype=torch.bfloat16, out=None, workspace="auto") -> torch.Tensor:
+    """y = silu(gate) * up [M, F] in 8-bit integers (see flashnorm_linear_int8); Q_gu int8 [2F, d] and scales [2F] from
+    flashnorm_fold_weights_int8(glu=True)."""
+    M, d, F = _int8_call(x, Q_gu, scales, True)
+    y = _output(out, (M, F), out_dtype, x)
+    if M == 0:
+        return y
+    ws = _call_workspace(workspace, flashnorm_int8_workspace_bytes(M, d, F, True, x.get_device()), x)
+    _invoke("flashnorm_glu_int8", x, _ptr(x), _ptr(Q_gu), _ptr(scales), _ptr(y), M, d, F, float(eps),
+            _out_code(out_dtype), _ptr(ws), ws.numel(), _stream_ptr(x))
     return y
 
 

@@ -20,8 +20,12 @@
 #include "fp8.cuh"
 #include "fused_gemm_pair.cuh"
 #include "gemv.cuh"
+#include "pair_gemm.cuh"
+#include "int8.cuh"
+#include "decode_int8.cuh"
 #include "postnorm_pair.cuh"
 #include "postnorm_split.cuh"
+#include "rope.cuh"
 
 namespace {
 
@@ -1439,3 +1443,8 @@ const char* flashnorm_last_error(void) { return g_last_error; }
 int flashnorm_version(void) { return 100; }
 
 }  // extern "C"
+
+// Host sides kept with their operators; they use the checks, maps and launch helpers above.
+#include "api_pair_gemm.cuh"
+#include "api_int8.cuh"
+#include "api_rope.cuh"

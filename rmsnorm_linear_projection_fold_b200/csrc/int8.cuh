@@ -1,0 +1,268 @@
+// int8.cuh — the W8A8 projection: 8-bit integer weights with one scale per output channel, activations quantized
+// on the fly to 8-bit integers with one scale per row, and the product between them exact in int32.
+//
+//     a[m]   = max_k |x[m, k]|,   q[m, k] = round(127 x[m, k] / a[m])        (ties to even; 0 for a row of zeros)
+//     rho[m] = a[m] / 127 / sqrt(mean_k x[m, k]^2 + eps)                      (no norm: a[m] / 127)
+//     s[n]   = max_k |g[k] W[k, n]| / 127,   Q[n, k] = round(g[k] W[k, n] / s[n])   (s = 1 for a channel of zeros)
+//     y[m, n] = rho[m] s[n] sum_k q[m, k] Q[n, k]
+// The deferred normalisation of "FlashNorm: Fast Normalization for Transformers" (Abstract, item ii) costs nothing
+// here: 1/rms is a row scalar, and so is the scale that any per-token quantization multiplies the product with.
+//
+// A call is a row pass (codes and rho, 3 bytes moved per element of x) and a product on kind::i8 tensor cores: CTA
+// pairs (pair_gemm.cuh) above 16 rows, the weight-streaming kernel of decode_int8.cuh up to 16.
+#pragma once
+
+#include "elementwise.cuh"
+#include "pair_gemm.cuh"
+
+namespace fn {
+
+// ---------------------------------------------------------------------------------------------- weights (offline)
+
+// s[row] of every output channel: 32 channels per block, eight k slices of each joined in shared memory. For GLU the
+// channel's row is the interleaved one (fold_dst_row).
+__global__ void __launch_bounds__(256) k_int8_scales(const uint16_t* __restrict__ W, const uint16_t* __restrict__ g,
+                                                     float* __restrict__ scales, int d, int N, int glu) {
+  __shared__ float part[8][32];
+  grid_dep_wait();
+  const int n = blockIdx.x * 32 + (threadIdx.x & 31), sl = threadIdx.x >> 5;
+  float amax = 0.0f;
+  if (n < N)
+    for (int k = sl; k < d; k += 8)
+      amax = fmaxf(amax, fabsf(bf16lo_to_f32(g[k]) * bf16lo_to_f32(W[static_cast<size_t>(k) * N + n])));
+  part[sl][threadIdx.x & 31] = amax;
+  __syncthreads();
+  if (sl == 0 && n < N) {
+    for (int i = 1; i < 8; ++i) amax = fmaxf(amax, part[i][threadIdx.x]);
+    scales[fold_dst_row(n, N / 2, glu != 0)] = amax > 0.0f ? __fdiv_rn(amax, 127.0f) : 1.0f;
+  }
+}
+
+// The codes, K-major: one 64 x 64 tile of W per block through shared memory, as k_fold does. d % 16 == 0, N % 8 == 0.
+__global__ void __launch_bounds__(256) k_fold_int8(const uint16_t* __restrict__ W, const uint16_t* __restrict__ g,
+                                                   const float* __restrict__ scales, int8_t* __restrict__ Q, int d,
+                                                   int N, int glu) {
+  __shared__ float tile[kFoldTile][kFoldTile + 1];  // [n][k]
+  const int k0 = blockIdx.y * kFoldTile, n0 = blockIdx.x * kFoldTile;
+  grid_dep_wait();
+  for (int i = threadIdx.x; i < kFoldTile * 8; i += 256) {
+    const int kk = i >> 3, ch = i & 7, k = k0 + kk, n = n0 + ch * 8;
+    if (k < d && n < N) {
+      const uint4 v = *reinterpret_cast<const uint4*>(W + static_cast<size_t>(k) * N + n);
+      const float gk = bf16lo_to_f32(g[k]);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        tile[ch * 8 + 2 * e][kk] = gk * bf16lo_to_f32(w[e]);  // exact: a bf16 x bf16 product fits fp32
+        tile[ch * 8 + 2 * e + 1][kk] = gk * bf16hi_to_f32(w[e]);
+      }
+    }
+  }
+  __syncthreads();
+  {  // one 16-byte store of 16 codes per thread
+    const int nn = threadIdx.x >> 2, ch = threadIdx.x & 3, n = n0 + nn, k = k0 + ch * 16;
+    if (n < N && k < d) {
+      const int row = fold_dst_row(n, N / 2, glu != 0);
+      const float s = scales[row];
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        w[e] = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int q = max(-127, min(127, __float2int_rn(__fdiv_rn(tile[nn][ch * 16 + 4 * e + j], s))));
+          w[e] |= (static_cast<uint32_t>(q) & 0xFFu) << (8 * j);
+        }
+      }
+      *reinterpret_cast<uint4*>(Q + static_cast<size_t>(row) * d + k) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------------------- the row pass
+
+// Code of x in a row of largest magnitude a: 127 x / a to the nearest integer, ties to even, decided exactly. inv is
+// fp32 127 / a, so |x| inv is within 2^-16 of the true quotient; only a value that near to a tie needs a second look,
+// at 254 |x| against (2 k + 1) a, both exact in double.
+__device__ __forceinline__ uint32_t int8_code(float x, float a, float inv) {
+  const float p = x * inv;
+  float q = rintf(p);
+  if (fabsf(fabsf(p - q) - 0.5f) < 1.0f / 8192.0f) {
+    const float k = floorf(fabsf(p));
+    const double l = 254.0 * static_cast<double>(fabsf(x)), r = (2.0 * static_cast<double>(k) + 1.0) * static_cast<double>(a);
+    const bool up = l > r || (l == r && (static_cast<int>(k) & 1));
+    q = copysignf(up ? k + 1.0f : k, x);
+  }
+  return static_cast<uint32_t>(static_cast<int>(q)) & 0xFFu;
+}
+
+// LPR threads per row, 256 / LPR rows per block; a thread keeps up to 4 x 8 elements of its row in registers, and a
+// longer row's remainder is read a second time (from L2). Also zeroes the `nzero` words at `zero`, the arrival
+// counters of a decode kernel that follows. A row with an infinity or a NaN gets zero codes and rho = NaN.
+// Bound: HBM, 2 bytes read and 1 written per element.
+template <int LPR>
+__global__ void __launch_bounds__(256) k_int8_rows(const uint16_t* __restrict__ x, int8_t* __restrict__ xq,
+                                                   float* __restrict__ rho, int M, int K, float eps, int norm,
+                                                   unsigned* __restrict__ zero, int nzero) {
+  constexpr int kHeld = 4;
+  constexpr int kWarps = LPR / 32;  // warps per row
+  __shared__ float red_s[8];
+  __shared__ uint32_t red_a[8];
+  grid_dep_wait();
+  grid_dep_launch();
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < nzero; i += 256) zero[i] = 0u;
+  const int sub = threadIdx.x % LPR, warp = threadIdx.x >> 5;
+  const int row = blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+  const bool live = row < M;
+  const uint4* src = reinterpret_cast<const uint4*>(x + static_cast<size_t>(live ? row : 0) * K);
+  const int chunks = live ? K >> 3 : 0;
+  uint4 held[kHeld];
+  float s0 = 0.f, s1 = 0.f;
+  uint32_t amax = 0;  // two 16-bit magnitudes
+  auto take = [&](const uint4& v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float lo = bf16lo_to_f32(w[e]), hi = bf16hi_to_f32(w[e]);
+      s0 = fmaf(lo, lo, s0);
+      s1 = fmaf(hi, hi, s1);
+      amax = __vmaxu2(amax, w[e] & 0x7FFF7FFFu);  // magnitudes order as unsigned bits, NaN above infinity
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int c = sub + i * LPR;
+    held[i] = c < chunks ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) take(held[i]);
+  for (int c = sub + kHeld * LPR; c < chunks; c += LPR) take(src[c]);
+  uint32_t am = max(amax & 0xFFFFu, amax >> 16);
+  float ss = s0 + s1;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
+  }
+  if (kWarps > 1) {
+    if ((threadIdx.x & 31) == 0) {
+      red_s[warp] = ss;
+      red_a[warp] = am;
+    }
+    __syncthreads();
+    const int w0 = warp / kWarps * kWarps;
+    ss = red_s[w0];
+    am = red_a[w0];
+    for (int i = 1; i < kWarps; ++i) {
+      ss += red_s[w0 + i];
+      am = max(am, red_a[w0 + i]);
+    }
+  }
+  if (!live) return;
+  // tiny rows are scaled by 2^100 (exact) so that 127 / a does not overflow
+  float a = __uint_as_float(am << 16);
+  const bool finite = am < 0x7F80u;
+  const float up = a < 1e-30f ? 0x1p100f : 1.0f;
+  if (sub == 0) {
+    float r = __fdiv_rn(a, 127.0f);
+    if (norm) r *= 1.0f / sqrtf(ss / static_cast<float>(K) + eps);
+    rho[row] = finite ? r : __int_as_float(0x7fc00000);
+  }
+  a *= up;
+  const float inv = finite && a > 0.f ? __fdiv_rn(127.0f, a) : 0.0f;
+  uint2* dst = reinterpret_cast<uint2*>(xq + static_cast<size_t>(row) * K);
+  auto put = [&](int c, const uint4& v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[2] = {0u, 0u};
+    if (finite) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        o[e >> 1] |= int8_code(bf16lo_to_f32(w[e]) * up, a, inv) << (16 * (e & 1));
+        o[e >> 1] |= int8_code(bf16hi_to_f32(w[e]) * up, a, inv) << (16 * (e & 1) + 8);
+      }
+    }
+    dst[c] = make_uint2(o[0], o[1]);
+  };
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int c = sub + i * LPR;
+    if (c < chunks) put(c, held[i]);
+  }
+  for (int c = sub + kHeld * LPR; c < chunks; c += LPR) put(c, src[c]);
+}
+
+// ---------------------------------------------------------------------------------------------- epilogues
+
+// silu(g) u with the SFU's exp2 and reciprocal (relative error about 1e-6); g -> -inf gives -0.
+__device__ __forceinline__ float int8_swiglu(float g, float u) {
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-g * 1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+  return g * s * u;
+}
+
+struct Int8EpiParams {
+  void* y;            // [M][n_out]
+  const float* rho;   // [M]
+  const float* scale;  // [rows of Q]
+  int n_out;
+};
+
+// y = rho s acc, or for GLU silu(rho s_g acc_g) (rho s_u acc_u) with gate and up interleaved in blocks of 16 columns.
+template <bool GLU, bool OUT_F32>
+struct Int8Epi {
+  using Params = Int8EpiParams;
+  float rho;
+  __device__ __forceinline__ Int8Epi(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
+    rho = t.row0 + lane < p.M ? __ldcg(e.rho + t.row0 + lane) : 0.f;
+  }
+  __device__ __forceinline__ void run(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
+    constexpr int kOut = OUT_F32 ? 16 : 32;      // outputs of a staged block (64 bytes of a row)
+    constexpr int kAcc = GLU ? 2 * kOut : kOut;  // its accumulator columns
+    constexpr int kEsz = OUT_F32 ? 4 : 2;
+    for (int ch = (t.half + t.turn) & 1; ch * kAcc < t.width; ch += 2) {
+      const int c0 = ch * kAcc;
+      uint32_t v[kAcc / 16][16];
+#pragma unroll
+      for (int b = 0; b < kAcc / 16; ++b) tmem_ld16(t.t_row + c0 + 16 * b, v[b]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int b = 0; b < kAcc / 16; ++b) reg_fence16(v[b]);
+      const float4* sc = reinterpret_cast<const float4*>(e.scale + t.n0 + c0);
+#pragma unroll
+      for (int b = 0; b < kAcc / 16; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          // N % 8 == 0: a group of four channels is wholly inside or wholly outside
+          const float4 s4 = c0 + 16 * b + 4 * j < t.width ? __ldg(sc + 4 * b + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[b][4 * j] = __float_as_uint(static_cast<float>(static_cast<int>(v[b][4 * j])) * rho * s4.x);
+          v[b][4 * j + 1] = __float_as_uint(static_cast<float>(static_cast<int>(v[b][4 * j + 1])) * rho * s4.y);
+          v[b][4 * j + 2] = __float_as_uint(static_cast<float>(static_cast<int>(v[b][4 * j + 2])) * rho * s4.z);
+          v[b][4 * j + 3] = __float_as_uint(static_cast<float>(static_cast<int>(v[b][4 * j + 3])) * rho * s4.w);
+        }
+      float o[kOut];
+#pragma unroll
+      for (int j = 0; j < kOut; ++j) {
+        if constexpr (GLU)
+          o[j] = int8_swiglu(__uint_as_float(v[2 * (j / 16)][j & 15]), __uint_as_float(v[2 * (j / 16) + 1][j & 15]));
+        else
+          o[j] = __uint_as_float(v[j / 16][j & 15]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (OUT_F32)
+          pg_put(t.stage, lane, j, make_uint4(__float_as_uint(o[4 * j]), __float_as_uint(o[4 * j + 1]),
+                                              __float_as_uint(o[4 * j + 2]), __float_as_uint(o[4 * j + 3])));
+        else
+          pg_put(t.stage, lane, j, make_uint4(pack_bf16x2(o[8 * j], o[8 * j + 1]), pack_bf16x2(o[8 * j + 2], o[8 * j + 3]),
+                                              pack_bf16x2(o[8 * j + 4], o[8 * j + 5]), pack_bf16x2(o[8 * j + 6], o[8 * j + 7])));
+      }
+      const int oc0 = GLU ? (t.n0 + c0) / 2 : t.n0 + c0;
+      pg_flush(t.stage, lane, e.y, static_cast<size_t>(e.n_out) * kEsz, t.row0, p.M, static_cast<long long>(oc0) * kEsz,
+               static_cast<long long>(e.n_out) * kEsz);
+    }
+  }
+};
+
+}  // namespace fn

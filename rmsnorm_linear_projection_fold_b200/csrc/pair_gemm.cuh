@@ -1,0 +1,344 @@
+// pair_gemm.cuh — the persistent CTA-pair matrix product (tcgen05 cta_group::2) behind the 8-bit integer
+// projection and the vocabulary head: C = A . B^T with one epilogue functor per use.
+//
+// Two CTAs of a cluster share each MMA of M = 256 rows: each stages its own 128 rows of A and half of the tile's
+// B rows (TMA into a ring of 128-byte-swizzled stages), the leader issues the MMAs, and each CTA's tensor memory
+// holds the accumulator of its own 128 rows (two of them, so that a tile's epilogue runs under the next tile's
+// MMAs). Unlike the deferred-norm kernel of fused_gemm_pair.cuh no warps read the staged x tiles: row statistics
+// come from a row pass before, which these operators need anyway (8-bit codes, 1/rms of the head). A tile may
+// therefore go to any pair, and pairs take tiles round robin in bands of `band` row tiles, row tile fastest: the
+// pairs running at one moment cover a compact block of C and share its A and B tiles in L2.
+//
+// Operands. bf16 (kind::f16, fp32 accumulator) or int8 (kind::i8, exact int32 accumulator); a stage holds 128
+// bytes of K per row (64 bf16, 128 int8). A bf16 operand may also be "MN-major": stored [K][rows], as a
+// transposed factor of a gradient is; its stage is boxes of 64 k x 64 rows, each 64 lines of 128 bytes.
+//
+// Warps: 0 = TMA producer, 1 = MMA issuer (leader) and tensor memory, 2..9 = epilogue, two per lane quarter.
+#pragma once
+
+#include "sm100.cuh"
+
+namespace fn {
+
+constexpr int kPgStages = 6;
+constexpr int kPgTileBytes = 16 * 1024;  // A or B of one stage: 128 rows x 128 bytes
+constexpr int kPgThreads = 320;
+constexpr int kPgOutBytes = 32 * 64;     // per epilogue warp: 32 rows x 64 bytes on their way out
+
+__host__ __device__ constexpr int pair_gemm_smem_bytes() {
+  return 1024 + kPgStages * 2 * kPgTileBytes + 8 * kPgOutBytes + 1024;
+}
+
+struct PairGemmParams {
+  int M, N;         // rows and columns of C
+  int num_kb;       // stages along K
+  int bn;           // tile width: a multiple of 32, at most 256
+  int num_m_tiles;  // of 256 rows
+  int num_n_tiles;
+  int band;         // row tiles per band
+  int ksplit;       // K ranges; range z of a tile goes to the epilogue as plane z
+};
+
+enum PgKind { PG_BF16 = 0, PG_I8 = 1 };
+
+// kind::i8 on a CTA pair, int32 accumulate.
+__device__ __forceinline__ void tc_mma_i8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor for kind::i8: signed 8-bit A and B, K-major, int32 D, shape M x N.
+__host__ __device__ constexpr uint32_t make_idesc_i8(int m, int n) {
+  return (2u << 4)                                // D format: s32
+         | (1u << 7)                              // A format: s8
+         | (1u << 10)                             // B format: s8
+         | (static_cast<uint32_t>(n >> 3) << 17)  // N / 8
+         | (static_cast<uint32_t>(m >> 4) << 24);  // M / 16
+}
+
+// Matrix descriptor of an MN-major operand: 64-wide blocks of 64 k lines (128 bytes each, 128-byte swizzle over
+// groups of 8 lines); the next block of 64 rows is 8 KB on (leading byte offset), the next 8 k 1 KB on (stride
+// byte offset).
+__device__ __forceinline__ uint64_t make_sdesc_mn_sw128(uint32_t smem_addr) {
+  return static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(8192 >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// What an epilogue warp works on: 32 rows of one tile (row0 + lane is this thread's) and columns col0 .. of it.
+struct PgTile {
+  uint32_t t_row;  // tensor-memory address of this warp's lanes, accumulator column 0
+  int row0;        // first row of the warp's lane quarter
+  int n0, width;   // the tile's columns
+  int half;        // which of the quarter's two warps
+  int turn;        // tile counter of this pair: the warps swap chunks from tile to tile
+  int nt, kz;      // column tile and K range
+  uint8_t* stage;  // this warp's staging buffer
+};
+
+// Copy a staged block of 32 rows x 64 bytes out, 8 rows x 64 bytes per warp store. `y` is the tensor, `ldb` its
+// row stride in bytes, `colb` the block's first column in bytes, `endb` the row's length in bytes (a multiple of
+// 16). The block was staged by pg_put: 16-byte piece j of row r at r * 64 + ((j ^ (r >> 1)) & 3) * 16.
+__device__ __forceinline__ void pg_put(uint8_t* stage, int lane, int j, uint4 v) {
+  *reinterpret_cast<uint4*>(stage + lane * 64 + (((j ^ (lane >> 1)) & 3) << 4)) = v;
+}
+__device__ __forceinline__ void pg_flush(uint8_t* stage, int lane, void* y, size_t ldb, int row0, int M, long long colb,
+                                         long long endb) {
+  __syncwarp();
+  const int seg = lane & 3;
+  const long long at = colb + seg * 16;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int rr = 8 * i + (lane >> 2);
+    const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 64 + (((seg ^ (rr >> 1)) & 3) << 4));
+    if (row0 + rr < M && at < endb)
+      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(y) + static_cast<size_t>(row0 + rr) * ldb + at) = v;
+  }
+  __syncwarp();  // the staging buffer is read before the next block overwrites it
+}
+
+template <int KIND, bool A_MN, bool B_MN, class Epi>
+__global__ void __launch_bounds__(kPgThreads, 1)
+    k_pair_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, PairGemmParams p,
+                typename Epi::Params ep) {
+  static_assert(KIND == PG_BF16 || (!A_MN && !B_MN), "8-bit operands are K-major");
+  constexpr int kElem = KIND == PG_I8 ? 1 : 2;
+  constexpr int kK = 128 / kElem;  // k per stage
+
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + kPgStages * kPgTileBytes;
+  uint8_t* sOut = sB + kPgStages * kPgTileBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sOut + 8 * kPgOutBytes);  // used in the leader
+  uint64_t* empty = full + kPgStages;
+  uint64_t* acc_full = empty + kPgStages;  // [2]
+  uint64_t* acc_empty = acc_full + 2;      // [2], used in the leader
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);
+  const int lane = static_cast<int>(threadIdx.x) & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPgStages; ++s) {
+      mbar_init(&full[s], 1);   // the leader's expect-tx arrival covers both CTAs' bytes
+      mbar_init(&empty[s], 1);  // the MMA's commit (multicast to both CTAs)
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 16);  // eight epilogue warps of each CTA
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_b);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers exist before either touches the other's
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  grid_dep_wait();  // the previous kernel's outputs (our inputs, or buffers we overwrite) are complete
+
+  const int cl = static_cast<int>(blockIdx.x) >> 1, ncl = static_cast<int>(gridDim.x) >> 1;
+  const int tiles = p.num_m_tiles * p.num_n_tiles;
+  const int items = tiles * p.ksplit;
+  // Item t: its row and column tile (bands of p.band row tiles, row tile fastest) and K range.
+  auto item_at = [&](int t, int& mt, int& nt, int& kz, int& kb0, int& kb1) {
+    kz = t / tiles;
+    const int u = t - kz * tiles;
+    const int per_band = p.band * p.num_n_tiles;
+    const int b = u / per_band, r = u - b * per_band;
+    const int rows = min(p.band, p.num_m_tiles - b * p.band);
+    mt = b * p.band + r % rows;
+    nt = r / rows;
+    kb0 = static_cast<int>(static_cast<long long>(kz) * p.num_kb / p.ksplit);
+    kb1 = static_cast<int>(static_cast<long long>(kz + 1) * p.num_kb / p.ksplit);
+  };
+  const int bh = p.bn / 2;                // B rows per CTA
+  const int b_boxes = (bh + 63) / 64;     // MN-major: 64-wide boxes per CTA
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer (both CTAs)
+    if (lane == 0) {
+      int s = 0, issued = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      const uint32_t stage_bytes =
+          static_cast<uint32_t>(kPgTileBytes + (B_MN ? b_boxes * 8192 : bh * 128));
+      for (int t = cl; t < items && ok; t += ncl) {
+        int mt, nt, kz, kb0, kb1;
+        item_at(t, mt, nt, kz, kb0, kb1);
+        const int m0 = mt * 256 + static_cast<int>(rank) * 128;
+        const int n0 = nt * p.bn + static_cast<int>(rank) * bh;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait_cluster(&empty[s], ph ^ 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t leader_full = dsmem_addr(&full[s], 0);
+          if (leader) mbar_arrive_expect_tx(&full[s], 2 * stage_bytes);
+          if (A_MN) {
+            tma_load_2d_pair(sA + s * kPgTileBytes, &tm_a, leader_full, m0, kb * kK);
+            tma_load_2d_pair(sA + s * kPgTileBytes + 8192, &tm_a, leader_full, m0 + 64, kb * kK);
+          } else {
+            tma_load_2d_pair(sA + s * kPgTileBytes, &tm_a, leader_full, kb * kK, m0);
+          }
+          if (B_MN) {
+            for (int j = 0; j < b_boxes; ++j)
+              tma_load_2d_pair(sB + s * kPgTileBytes + j * 8192, &tm_b, leader_full, n0 + 64 * j, kb * kK);
+          } else {
+            tma_load_2d_pair(sB + s * kPgTileBytes, &tm_b, leader_full, kb * kK, n0);
+          }
+          ++issued;
+          if (++s == kPgStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      grid_dep_launch();  // all loads issued: the next kernel may be scheduled onto SMs as they free up
+      if (ok) {
+        // The release of the last use of every stage, so that no arrival on this CTA's barriers (an MMA commit
+        // completes asynchronously) is still in flight when the CTA exits.
+        for (int i = 0; i < kPgStages; ++i) {
+          if (!mbar_wait_cluster(&empty[s], ph ^ 1u, abort_flag)) break;
+          if (++s == kPgStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (!ok && leader) {
+        // Gave up: let the pair's copies still in flight land (bounded) before shared memory goes.
+        const int pending = issued < kPgStages ? issued : kPgStages;
+        for (int i = 1; i <= pending; ++i) {
+          int st = s - i;
+          uint32_t pp = ph;
+          if (st < 0) {
+            st += kPgStages;
+            pp ^= 1u;
+          }
+          const unsigned long long t0 = globaltimer_ns();
+          while (!mbar_try_wait_cluster(&full[st], pp) && globaltimer_ns() - t0 < kWaitLimitNs) {
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ pair MMA issuer (leader)
+    if (lane == 0 && leader) {
+      const uint32_t idesc = KIND == PG_I8 ? make_idesc_i8(256, p.bn)
+                                           : make_idesc_bf16(256, p.bn) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+      int s = 0;
+      uint32_t ph = 0;
+      int acc = 0;
+      uint32_t acc_ph = 0;
+      bool ok = true;
+      for (int t = cl; t < items && ok; t += ncl) {
+        int mt, nt, kz, kb0, kb1;
+        item_at(t, mt, nt, kz, kb0, kb1);
+        if (!mbar_wait_cluster(&acc_empty[acc], acc_ph ^ 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 256);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait_cluster(&full[s], ph, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t a_addr = smem_u32(sA + s * kPgTileBytes);
+          const uint32_t b_addr = smem_u32(sB + s * kPgTileBytes);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // K-major: 32 bytes of every row; MN-major: 16 lines
+            const uint64_t da = A_MN ? make_sdesc_mn_sw128(a_addr + k * 2048) : make_sdesc_sw128(a_addr + k * 32);
+            const uint64_t db = B_MN ? make_sdesc_mn_sw128(b_addr + k * 2048) : make_sdesc_sw128(b_addr + k * 32);
+            const uint32_t accumulate = (kb != kb0 || k != 0) ? 1u : 0u;
+            if (KIND == PG_I8)
+              tc_mma_i8_pair(d_tmem, da, db, idesc, accumulate);
+            else
+              tc_mma_bf16_pair(d_tmem, da, db, idesc, accumulate);
+          }
+          tc_commit_pair_mc(&empty[s], 0x3);  // frees stage s in both CTAs once read
+          if (++s == kPgStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (!ok) break;
+        tc_commit_pair_mc(&acc_full[acc], 0x3);
+        acc ^= 1;
+        if (acc == 0) acc_ph ^= 1u;
+      }
+      if (!ok) {
+        tc_commit_pair_mc(drain, 0x1);
+        const unsigned long long t0 = globaltimer_ns();
+        while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ epilogue (both CTAs)
+    const int q = warp & 3;
+    const uint32_t leader_acc_empty0 = dsmem_addr(&acc_empty[0], 0);
+    const uint32_t leader_acc_empty1 = dsmem_addr(&acc_empty[1], 0);
+    int acc = 0, turn = 0;
+    uint32_t acc_ph = 0;
+    for (int t = cl; t < items; t += ncl, ++turn) {
+      int mt, nt, kz, kb0, kb1;
+      item_at(t, mt, nt, kz, kb0, kb1);
+      PgTile tile;
+      tile.row0 = mt * 256 + static_cast<int>(rank) * 128 + q * 32;
+      tile.n0 = nt * p.bn;
+      tile.width = min(p.bn, p.N - tile.n0);
+      tile.half = (warp - 2) >> 2;
+      tile.turn = turn;
+      tile.nt = nt;
+      tile.kz = kz;
+      tile.stage = sOut + (warp - 2) * kPgOutBytes;
+      tile.t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * 256);
+      Epi epi(ep, p, tile, lane);  // row parameters are on their way while the MMAs finish
+      if (!mbar_wait_cluster(&acc_full[acc], acc_ph, abort_flag)) break;
+      tc_fence_after_sync();
+      epi.run(ep, p, tile, lane);
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (leader)
+          mbar_arrive(&acc_empty[acc]);
+        else
+          mbar_arrive_remote(acc == 0 ? leader_acc_empty0 : leader_acc_empty1);
+      }
+      acc ^= 1;
+      if (acc == 0) acc_ph ^= 1u;
+    }
+  }
+
+  // ------------------------------------------------------------------ teardown
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync_all();  // no CTA leaves while the other may still signal its barriers
+  tc_fence_after_sync();
+  if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
+}
+
+}  // namespace fn

@@ -321,3 +321,81 @@ def test_nvfp4_validation(lib):
         nbytes.value = -7
         assert lib.flashnorm_nvfp4_workspace_bytes(*shape, out) == fn.FN_OK
         assert nbytes.value == 0
+
+
+# flashnorm_rope(x, cs, positions, y, M, H, head_dim, rot_dim, n_rope_heads, max_pos, x_row, x_head, y_row, y_head, layout,
+#                backward, dtype, stream): rejected on the host
+_ROPE_OK = dict(x=P, cs=P, pos=P, y=ctypes.c_void_p(1 << 24), M=4, H=2, hd=64, rot=32, n=2, max_pos=8, xr=128, xh=64, yr=128,
+                yh=64, layout=0, backward=0, dtype=0)
+
+
+@pytest.mark.parametrize("change,expected", [
+    (dict(M=-1), fn.FN_ERR_INVALID_ARG),
+    (dict(H=0), fn.FN_ERR_INVALID_ARG),
+    (dict(rot=31), fn.FN_ERR_INVALID_ARG),
+    (dict(rot=66), fn.FN_ERR_INVALID_ARG),
+    (dict(n=3), fn.FN_ERR_INVALID_ARG),
+    (dict(max_pos=0), fn.FN_ERR_INVALID_ARG),
+    (dict(layout=2), fn.FN_ERR_INVALID_ARG),
+    (dict(backward=2), fn.FN_ERR_INVALID_ARG),
+    (dict(dtype=3), fn.FN_ERR_INVALID_ARG),
+    (dict(yh=63), fn.FN_ERR_INVALID_ARG),                  # heads of y overlap
+    (dict(yr=127), fn.FN_ERR_INVALID_ARG),                 # rows of y overlap
+    (dict(yr=64, yh=255), fn.FN_ERR_INVALID_ARG),          # heads of rows, one element short
+    (dict(xr=-128), fn.FN_ERR_INVALID_ARG),
+    (dict(y=P, xr=256), fn.FN_ERR_INVALID_ARG),            # in place with different strides
+    (dict(x=NULL), fn.FN_ERR_INVALID_ARG),
+    (dict(pos=NULL), fn.FN_ERR_INVALID_ARG),
+    (dict(cs=P_MISALIGNED), fn.FN_ERR_ALIGN),
+    (dict(x=ctypes.c_void_p((1 << 20) + 1)), fn.FN_ERR_ALIGN),
+    (dict(M=0), fn.FN_OK),
+])
+def test_rope_validation(lib, change, expected):
+    a = {**_ROPE_OK, **change}
+    assert lib.flashnorm_rope(a["x"], a["cs"], a["pos"], a["y"], a["M"], a["H"], a["hd"], a["rot"], a["n"], a["max_pos"],
+                              a["xr"], a["xh"], a["yr"], a["yh"], a["layout"], a["backward"], a["dtype"], NULL) == expected
+
+
+@pytest.mark.parametrize("args", [
+    (0, 64, 1e4, 0, 1.0, 0.0, 1.0, 32.0, 1.0),       # empty
+    (8, 7, 1e4, 0, 1.0, 0.0, 1.0, 32.0, 1.0),        # odd rot_dim
+    (8, 64, 1.0, 0, 1.0, 0.0, 1.0, 32.0, 1.0),       # base
+    (8, 64, 1e4, 4, 1.0, 0.0, 1.0, 32.0, 1.0),       # unknown scaling
+    (8, 64, 1e4, 1, 0.5, 0.0, 1.0, 32.0, 1.0),       # factor < 1
+    (8, 2, 1e4, 2, 2.0, 0.0, 1.0, 32.0, 1.0),        # ntk needs rot_dim > 2
+    (8, 64, 1e4, 3, 2.0, 0.0, 1.0, 32.0, 1.0),       # yarn without the original length
+    (8, 64, 1e4, 3, 2.0, 4096.0, 32.0, 32.0, 1.0),   # alpha == beta
+    (8, 64, 1e4, 0, 1.0, 0.0, 1.0, 32.0, 0.0),       # attention factor
+    (8, 64, 1e4, 0, 1.0, 0.0, 1.0, 32.0, float("nan")),
+])
+def test_rope_table_scaled_validation(lib, args):
+    assert lib.flashnorm_rope_table_scaled(P, *args, NULL) == fn.FN_ERR_INVALID_ARG
+
+
+def test_int8_validation(lib):
+    lin, glu, size = lib.flashnorm_linear_int8, lib.flashnorm_glu_int8, lib.flashnorm_int8_workspace_bytes
+    big = 1 << 40
+    assert lin(P, P, P, P, -1, 576, 960, 1e-6, 1, 0, P, big, NULL) == fn.FN_ERR_INVALID_ARG
+    assert lin(P, P, P, P, 4, 584, 960, 1e-6, 1, 0, P, big, NULL) == fn.FN_ERR_INVALID_ARG       # d % 16
+    assert lin(P, P, P, P, 4, 576, 964, 1e-6, 1, 0, P, big, NULL) == fn.FN_ERR_INVALID_ARG       # N % 8
+    assert lin(P, P, P, P, 4, 131088, 960, 1e-6, 1, 0, P, big, NULL) == fn.FN_ERR_UNSUPPORTED    # int32 sums
+    assert lin(P, P, P, P, 4, 576, 960, -1.0, 1, 0, P, big, NULL) == fn.FN_ERR_INVALID_ARG
+    assert lin(P, P, P, P, 4, 576, 960, 1e-6, 2, 0, P, big, NULL) == fn.FN_ERR_INVALID_ARG       # norm flag
+    assert lin(P, P, P, P, 4, 576, 960, 1e-6, 1, 5, P, big, NULL) == fn.FN_ERR_INVALID_ARG       # out dtype
+    assert lin(P, NULL, P, P, 4, 576, 960, 1e-6, 1, 0, P, big, NULL) == fn.FN_ERR_INVALID_ARG
+    assert lin(P, P, P_MISALIGNED, P, 4, 576, 960, 1e-6, 1, 0, P, big, NULL) == fn.FN_ERR_ALIGN
+    assert lin(P, P, P, P, 4, 576, 960, 1e-6, 1, 0, NULL, 0, NULL) == fn.FN_ERR_INVALID_ARG      # no workspace
+    assert lin(P, P, P, P, 4, 576, 960, 1e-6, 1, 0, P, -1, NULL) == fn.FN_ERR_INVALID_ARG
+    assert lin(P, P, P, P, 0, 576, 960, 1e-6, 1, 0, NULL, 0, NULL) == fn.FN_OK                   # empty call
+    assert glu(P, P, P, P, 4, 576, 24, 1e-6, 0, P, big, NULL) == fn.FN_ERR_INVALID_ARG           # F % 16
+    fold = lib.flashnorm_fold_weights_int8
+    assert fold(P, P, P, P, 24, 64, 0, NULL) == fn.FN_ERR_INVALID_ARG
+    assert fold(P, P, P, P, 64, 48, 1, NULL) == fn.FN_ERR_INVALID_ARG
+    assert fold(P, P, P, P, 64, 64, 2, NULL) == fn.FN_ERR_INVALID_ARG
+    assert fold(P, P, NULL, P, 64, 64, 0, NULL) == fn.FN_ERR_INVALID_ARG
+    n = ctypes.c_int64(-7)
+    out = ctypes.c_void_p(ctypes.addressof(n))
+    assert size(4, 576, 960, 0, NULL) == fn.FN_ERR_INVALID_ARG
+    for shape in [(4, 584, 960, 0), (4, 576, 964, 0), (-1, 576, 960, 0), (4, 576, 24, 1), (4, 576, 960, 3)]:
+        assert size(*shape, out) == fn.FN_ERR_INVALID_ARG, shape
+    assert size(0, 576, 960, 0, out) == fn.FN_OK and n.value == 0
