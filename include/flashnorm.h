@@ -336,6 +336,38 @@ FN_API fn_status flashnorm_glu_int8(const void* x, const void* Q, const void* sc
                                     void* stream);
 FN_API fn_status flashnorm_int8_workspace_bytes(int64_t M, int64_t d, int64_t N, int glu, int64_t* bytes);
 
+/*
+ * Softmax cross entropy of the vocabulary head behind the final RMSNorm, and its gradient, without keeping the logits
+ * (the same Abstract items: the gain is folded into the head, 1/rms deferred):
+ *     r[m] = 1/sqrt(mean(x[m]^2) + eps),   l[m][n] = r[m] sum_k x[m][k] W*[n][k]
+ *     lse[m] = log sum_n exp(l[m][n]),     loss[m] = lse[m] - l[m][targets[m]]
+ * flashnorm_linear_cross_entropy: x bf16 [M, d], Wstar bf16 [V, d] (flashnorm_fold_weights), targets int64 [M] ->
+ *   loss and lse, fp32 [M]. A row whose target is ignore_index has loss 0 (its lse is computed all the same). A target
+ *   that is neither a class (0 .. V-1) nor ignore_index gives that row a NaN loss, and the next
+ *   flashnorm_check_device_error returns FN_ERR_INVALID_ARG.
+ * flashnorm_linear_cross_entropy_backward: g fp32 [M] (dL/dloss), x, Wstar, targets as above and the forward's lse ->
+ *   dx bf16 [M, d] and dWstar bf16 [V, d], both overwritten. With dl[m][n] = g[m] (exp(l[m][n] - lse[m]) - [n = t[m]]):
+ *     dW*[n] = sum_m r[m] dl[m][n] x[m],   dx[m] = r[m] sum_n dl[m][n] W*[n] - x[m] (r[m]^2 / d) sum_n dl[m][n] l[m][n]
+ *   Rows whose target is ignore_index have a zero dx and take no part in dW*; a bad target gives its row a NaN dx, takes
+ *   no part in dW* and is reported as above. r dl is rounded to bf16 once for the two products; sums are fp32. M == 0
+ *   sets dWstar to zero.
+ * flashnorm_cross_entropy_workspace_bytes: the scratch a call (backward: 0 or 1) of this shape needs on the current
+ *   device, written to *bytes; bounded by a piece of the vocabulary, not the whole. Caller-owned, 16-byte aligned,
+ *   contents irrelevant before and after; calls whose kernels may overlap on the GPU must not share one. A smaller one
+ *   returns FN_ERR_INVALID_ARG.
+ * Constraints: d % 8 == 0; any M and V.
+ */
+FN_API fn_status flashnorm_linear_cross_entropy(const void* x, const void* Wstar, const void* targets, void* loss,
+                                                void* lse, int64_t M, int64_t d, int64_t V, float eps,
+                                                int64_t ignore_index, void* workspace, int64_t workspace_bytes,
+                                                void* stream);
+FN_API fn_status flashnorm_linear_cross_entropy_backward(const void* g, const void* x, const void* Wstar,
+                                                         const void* targets, const void* lse, void* dx, void* dWstar,
+                                                         int64_t M, int64_t d, int64_t V, float eps,
+                                                         int64_t ignore_index, void* workspace,
+                                                         int64_t workspace_bytes, void* stream);
+FN_API fn_status flashnorm_cross_entropy_workspace_bytes(int64_t M, int64_t d, int64_t V, int backward, int64_t* bytes);
+
 /* Which features of a head form a rotated pair: (2i, 2i + 1), or (i, i + rot_dim / 2). */
 typedef enum { FN_ROPE_INTERLEAVED = 0, FN_ROPE_HALF = 1 } fn_rope_layout;
 

@@ -47,6 +47,9 @@ __all__ = [
     "flashnorm_int8_workspace_bytes",
     "flashnorm_rope",
     "flashnorm_rope_table_scaled",
+    "flashnorm_linear_cross_entropy",
+    "flashnorm_linear_cross_entropy_backward",
+    "flashnorm_cross_entropy_workspace_bytes",
     "flashnorm_layernorm_linear",
     "flashnorm_rmsnorm",
     "flashnorm_linear_unfused",
@@ -102,6 +105,9 @@ _SIGNATURES = {
     "flashnorm_int8_workspace_bytes": [_I64, _I64, _I64, _INT, _P],
     "flashnorm_rope": [_P, _P, _P, _P] + [_I64] * 10 + [_INT, _INT, _INT, _P],
     "flashnorm_rope_table_scaled": [_P, _I64, _I64, _D, _INT, _D, _D, _D, _D, _D, _P],
+    "flashnorm_linear_cross_entropy": [_P, _P, _P, _P, _P, _I64, _I64, _I64, _F, _I64, _P, _I64, _P],
+    "flashnorm_linear_cross_entropy_backward": [_P] * 7 + [_I64, _I64, _I64, _F, _I64, _P, _I64, _P],
+    "flashnorm_cross_entropy_workspace_bytes": [_I64, _I64, _I64, _INT, _P],
     "flashnorm_layernorm_linear": [_P, _P, _P, _P, _P, _I64, _I64, _I64, _F, _INT, _P],
     "flashnorm_rmsnorm": [_P, _P, _P, _I64, _I64, _F, _P],
     "flashnorm_linear_unfused": [_P, _P, _P, _P, _P, _I64, _I64, _I64, _F, _INT, _P],
@@ -789,6 +795,77 @@ def flashnorm_glu_int8(x: torch.Tensor, Q_gu: torch.Tensor, scales: torch.Tensor
     _invoke("flashnorm_glu_int8", x, _ptr(x), _ptr(Q_gu), _ptr(scales), _ptr(y), M, d, F, float(eps),
             _out_code(out_dtype), _ptr(ws), ws.numel(), _stream_ptr(x))
     return y
+
+
+_ce_ws_bytes_cache = {}
+
+
+def flashnorm_cross_entropy_workspace_bytes(M: int, d: int, V: int, backward: bool = False, device=None) -> int:
+    """Workspace bytes flashnorm_linear_cross_entropy (or its backward) needs for this shape on `device`."""
+    dev = torch.cuda.current_device() if device is None else torch.device(device).index
+    if dev is None:
+        dev = torch.cuda.current_device()
+    key = (dev, M, d, V, backward)
+    hit = _ce_ws_bytes_cache.get(key)
+    if hit is not None:
+        return hit
+    nbytes = ctypes.c_int64(0)
+    _invoke_on(dev, "flashnorm_cross_entropy_workspace_bytes", int(M), int(d), int(V), int(bool(backward)),
+               ctypes.addressof(nbytes))
+    if len(_ce_ws_bytes_cache) >= 4096:
+        _ce_ws_bytes_cache.clear()
+    _ce_ws_bytes_cache[key] = int(nbytes.value)
+    return int(nbytes.value)
+
+
+def _ce_call(x, Wstar, targets):
+    _need(x, "x", dim=2)
+    _need(Wstar, "Wstar", dim=2)
+    _need(targets, "targets", torch.int64, dim=1)
+    M, d = x.shape
+    if Wstar.shape[1] != d:
+        raise ValueError("Wstar must be [V, d] with the d of x")
+    if targets.shape[0] != M:
+        raise ValueError("targets must have one entry per row of x")
+    _same_device(x, Wstar=Wstar, targets=targets)
+    return M, d, Wstar.shape[0]
+
+
+def flashnorm_linear_cross_entropy(x: torch.Tensor, Wstar: torch.Tensor, targets: torch.Tensor, eps: float,
+                                   ignore_index: int = -100, workspace="auto"):
+    """(loss, lse), fp32 [M]: softmax cross entropy of the logits r x . W* (final RMSNorm, then the vocabulary head),
+    which are never stored. x [M, d] bf16, W* [V, d] bf16 from fold_weights, targets int64 [M]; a row whose target is
+    ignore_index has loss 0. workspace: "auto", or a uint8 CUDA tensor of at least
+    flashnorm_cross_entropy_workspace_bytes(M, d, V) bytes."""
+    M, d, V = _ce_call(x, Wstar, targets)
+    loss = torch.empty(M, dtype=torch.float32, device=x.device)
+    lse = torch.empty(M, dtype=torch.float32, device=x.device)
+    if M == 0:
+        return loss, lse
+    ws = _call_workspace(workspace, flashnorm_cross_entropy_workspace_bytes(M, d, V, False, x.get_device()), x)
+    _invoke("flashnorm_linear_cross_entropy", x, _ptr(x), _ptr(Wstar), _ptr(targets), _ptr(loss), _ptr(lse), M, d, V,
+            float(eps), int(ignore_index), _ptr(ws), ws.numel(), _stream_ptr(x))
+    return loss, lse
+
+
+def flashnorm_linear_cross_entropy_backward(grad_loss: torch.Tensor, x: torch.Tensor, Wstar: torch.Tensor,
+                                            targets: torch.Tensor, lse: torch.Tensor, eps: float,
+                                            ignore_index: int = -100, workspace="auto"):
+    """(dx [M, d], dWstar [V, d]), bf16: the gradient of flashnorm_linear_cross_entropy's losses weighted with grad_loss
+    (fp32 [M]); lse is the forward's. The logits are computed again in pieces of the vocabulary. workspace: "auto", or
+    a uint8 CUDA tensor of at least flashnorm_cross_entropy_workspace_bytes(M, d, V, backward=True) bytes."""
+    M, d, V = _ce_call(x, Wstar, targets)
+    _need(grad_loss, "grad_loss", torch.float32, dim=1)
+    _need(lse, "lse", torch.float32, dim=1)
+    if grad_loss.shape[0] != M or lse.shape[0] != M:
+        raise ValueError("grad_loss and lse must have one entry per row of x")
+    _same_device(x, grad_loss=grad_loss, lse=lse)
+    dx = torch.empty_like(x)
+    dW = torch.empty_like(Wstar)
+    ws = _call_workspace(workspace, flashnorm_cross_entropy_workspace_bytes(M, d, V, True, x.get_device()), x)
+    _invoke("flashnorm_linear_cross_entropy_backward", x, _ptr(grad_loss), _ptr(x), _ptr(Wstar), _ptr(targets),
+            _ptr(lse), _ptr(dx), _ptr(dW), M, d, V, float(eps), int(ignore_index), _ptr(ws), ws.numel(), _stream_ptr(x))
+    return dx, dW
 
 
 def flashnorm_rmsnorm(x: torch.Tensor, g: torch.Tensor, eps: float, out=None) -> torch.Tensor:

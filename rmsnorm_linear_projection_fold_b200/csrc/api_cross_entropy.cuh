@@ -1,0 +1,230 @@
+// api_cross_entropy.cuh — host side of the vocabulary head's cross entropy and its gradient (cross_entropy.cuh). Part of
+// flashnorm.cu.
+#pragma once
+
+namespace {
+
+// 2-D bf16 operand stored MN-major, [k][cols] with row stride ld: 64 cols x 64 k boxes, 128-byte swizzle.
+fn_status make_mn_map(CUtensorMap* map, const void* ptr, int64_t cols, int64_t k, int64_t ld) {
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(k)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  cuuint32_t box[2] = {64u, 64u};
+  CUresult r = encode_cached(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box,
+                             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+  if (r == CUDA_ERROR_NOT_FOUND) return fail(FN_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  if (r != CUDA_SUCCESS) return fail(FN_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
+  return FN_OK;
+}
+
+// 2-D bf16 K-major operand [rows][k] with row stride ld: 64 k x box_rows boxes, 128-byte swizzle.
+fn_status make_k_map(CUtensorMap* map, const void* ptr, int64_t k, int64_t rows, int64_t ld, int box_rows) {
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  cuuint32_t box[2] = {64u, static_cast<cuuint32_t>(box_rows)};
+  CUresult r = encode_cached(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box,
+                             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+  if (r == CUDA_ERROR_NOT_FOUND) return fail(FN_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  if (r != CUDA_SUCCESS) return fail(FN_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
+  return FN_OK;
+}
+
+// What a call works through and where the parts of its workspace start.
+struct CePlan {
+  int64_t piece;   // vocabulary columns of a piece (forward: all)
+  int64_t pieces;
+  int n_tiles;     // column tiles of a full piece
+  int ksplit;      // K ranges of dx's product
+  int64_t rstd, part, tlogit, P, acc, bytes;
+};
+
+constexpr int64_t kCePieceBytes = int64_t{64} << 20;  // of P, per piece
+
+CePlan ce_plan(int64_t M, int64_t d, int64_t V, bool backward, int sms) {
+  CePlan c = {};
+  c.piece = V, c.pieces = 1, c.ksplit = 1;
+  if (backward) {
+    const int64_t cap = std::max<int64_t>(2048, kCePieceBytes / (2 * M) / 256 * 256);
+    c.pieces = (V + cap - 1) / cap;
+    c.piece = c.pieces == 1 ? V : round_up((V + c.pieces - 1) / c.pieces, 256);
+    c.pieces = (V + c.piece - 1) / c.piece;
+  }
+  fn::PairGemmParams g;
+  plan_pair_gemm(&g, M, c.piece, (d + 63) / 64, sms, 32, 1);
+  c.n_tiles = g.num_n_tiles;
+  c.rstd = 0;
+  c.part = round_up(4 * M, 256);
+  if (!backward) {
+    c.tlogit = c.part + round_up(16ll * c.n_tiles * M, 256);
+    c.bytes = c.tlogit + round_up(4 * M, 256);
+    return c;
+  }
+  const int64_t num_kb = (c.piece + 63) / 64;
+  plan_pair_gemm(&g, M, d, num_kb, sms, 32, 1);
+  const int64_t tiles = static_cast<int64_t>(g.num_m_tiles) * g.num_n_tiles;
+  c.ksplit = static_cast<int>(std::max<int64_t>(1, std::min(sms / 2 / tiles, num_kb / 8)));
+  c.P = c.part + round_up(8ll * c.n_tiles * c.pieces * M, 256);
+  c.acc = c.P + round_up(2 * M * round_up(c.piece, 8), 256);
+  c.bytes = c.acc + 4 * c.ksplit * M * d;
+  return c;
+}
+
+fn_status check_ce_shape(int64_t M, int64_t d, int64_t V) {
+  if (M < 0 || M > kMaxDim) return fail(FN_ERR_INVALID_ARG, "M = %lld out of range", (long long)M);
+  if (d < 8 || d > kMaxDim || d % 8 != 0) return fail(FN_ERR_INVALID_ARG, "d = %lld must be a positive multiple of 8", (long long)d);
+  if (V < 1 || V > kMaxDim / 2) return fail(FN_ERR_INVALID_ARG, "V = %lld out of range", (long long)V);
+  return FN_OK;
+}
+
+fn_status check_ce_call(const void* x, const void* w, const void* targets, const void* a, const char* an, const void* b,
+                        const char* bn, float eps, const void* workspace, int64_t workspace_bytes) {
+  fn_status st;
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(FN_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (workspace_bytes < 0) return fail(FN_ERR_INVALID_ARG, "workspace_bytes < 0");
+  if ((st = check_ptr(x, "x")) != FN_OK) return st;
+  if ((st = check_ptr(w, "W*")) != FN_OK) return st;
+  if ((st = check_ptr(targets, "targets")) != FN_OK) return st;
+  if ((st = check_ptr(a, an)) != FN_OK) return st;
+  if ((st = check_ptr(b, bn)) != FN_OK) return st;
+  return check_ptr(workspace, "workspace");
+}
+
+fn_status launch_rstd(const void* x, float* rstd, int64_t M, int64_t d, float eps, cudaStream_t s) {
+  cudaError_t e = launch_kernel(fn::k_row_rstd, dim3(static_cast<unsigned>((M + 7) / 8)), dim3(256), 0, s, 1,
+                                static_cast<const uint16_t*>(x), rstd, static_cast<int>(M), static_cast<int>(d), eps);
+  return e == cudaSuccess ? FN_OK : cuda_fail(e, "row statistics launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+fn_status flashnorm_cross_entropy_workspace_bytes(int64_t M, int64_t d, int64_t V, int backward, int64_t* bytes) {
+  g_last_error[0] = '\0';
+  if (bytes == nullptr) return fail(FN_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = 0;
+  if (backward != 0 && backward != 1) return fail(FN_ERR_INVALID_ARG, "backward must be 0 or 1");
+  fn_status st = check_ce_shape(M, d, V);
+  if (st != FN_OK || M == 0) return st;
+  int dev = 0;
+  const int sms = device_sm_count(&dev);
+  if (sms <= 1) return fail(FN_ERR_CUDA, "cannot query the current device");
+  *bytes = ce_plan(M, d, V, backward != 0, sms).bytes;
+  return FN_OK;
+}
+
+fn_status flashnorm_linear_cross_entropy(const void* x, const void* Wstar, const void* targets, void* loss, void* lse,
+                                         int64_t M, int64_t d, int64_t V, float eps, int64_t ignore_index,
+                                         void* workspace, int64_t workspace_bytes, void* stream) {
+  g_last_error[0] = '\0';
+  fn_status st = check_ce_shape(M, d, V);
+  if (st != FN_OK || M == 0) return st;
+  if ((st = check_ce_call(x, Wstar, targets, loss, "loss", lse, "lse", eps, workspace, workspace_bytes)) != FN_OK) return st;
+  int dev = 0;
+  const int sms = device_sm_count(&dev);
+  if (sms <= 1) return fail(FN_ERR_CUDA, "cannot query the current device");
+  const CePlan c = ce_plan(M, d, V, false, sms);
+  if (workspace_bytes < c.bytes)
+    return fail(FN_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes, (long long)c.bytes);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  float* rstd = reinterpret_cast<float*>(base + c.rstd);
+  fn::CeFwdParams ep;
+  ep.rstd = rstd;
+  ep.targets = static_cast<const long long*>(targets);
+  ep.part = reinterpret_cast<float2*>(base + c.part);
+  ep.tlogit = reinterpret_cast<float*>(base + c.tlogit);
+  fn::PairGemmParams p;
+  plan_pair_gemm(&p, M, V, (d + 63) / 64, sms, 32, 1);
+  CUtensorMap tx, tw;
+  if ((st = make_k_map(&tx, x, d, M, d, 128)) != FN_OK) return st;
+  if ((st = make_k_map(&tw, Wstar, d, V, d, p.bn / 2)) != FN_OK) return st;
+  if ((st = launch_rstd(x, rstd, M, d, eps, s)) != FN_OK) return st;
+  if ((st = launch_pair_gemm<fn::PG_BF16, false, false, fn::CeFwdEpi>(tx, tw, p, ep, sms, dev, s, "cross entropy GEMM")) != FN_OK)
+    return st;
+  cudaError_t e = launch_kernel(fn::k_ce_join, dim3(static_cast<unsigned>((M + 31) / 32)), dim3(256), 0, s, 1,
+                                static_cast<const float2*>(ep.part), static_cast<const float*>(ep.tlogit), ep.targets,
+                                static_cast<float*>(loss), static_cast<float*>(lse), p.M, p.N, 2 * p.num_n_tiles,
+                                static_cast<long long>(ignore_index));
+  return e == cudaSuccess ? FN_OK : cuda_fail(e, "cross entropy join launch");
+}
+
+fn_status flashnorm_linear_cross_entropy_backward(const void* g, const void* x, const void* Wstar, const void* targets,
+                                                  const void* lse, void* dx, void* dWstar, int64_t M, int64_t d,
+                                                  int64_t V, float eps, int64_t ignore_index, void* workspace,
+                                                  int64_t workspace_bytes, void* stream) {
+  g_last_error[0] = '\0';
+  fn_status st = check_ce_shape(M, d, V);
+  if (st != FN_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M == 0) {  // no rows: the weight's gradient is zero
+    if ((st = check_ptr(dWstar, "dW*")) != FN_OK) return st;
+    cudaError_t e = cudaMemsetAsync(dWstar, 0, static_cast<size_t>(V) * static_cast<size_t>(d) * 2, s);
+    return e == cudaSuccess ? FN_OK : cuda_fail(e, "clearing dW*");
+  }
+  if ((st = check_ce_call(x, Wstar, targets, g, "g", lse, "lse", eps, workspace, workspace_bytes)) != FN_OK) return st;
+  if ((st = check_ptr(dx, "dx")) != FN_OK) return st;
+  if ((st = check_ptr(dWstar, "dW*")) != FN_OK) return st;
+  int dev = 0;
+  const int sms = device_sm_count(&dev);
+  if (sms <= 1) return fail(FN_ERR_CUDA, "cannot query the current device");
+  const CePlan c = ce_plan(M, d, V, true, sms);
+  if (workspace_bytes < c.bytes)
+    return fail(FN_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes, (long long)c.bytes);
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  float* rstd = reinterpret_cast<float*>(base + c.rstd);
+  float* cpart = reinterpret_cast<float*>(base + c.part);
+  uint16_t* P = reinterpret_cast<uint16_t*>(base + c.P);
+  float* acc = reinterpret_cast<float*>(base + c.acc);
+  const int64_t ldp = round_up(c.piece, 8);
+  if ((st = launch_rstd(x, rstd, M, d, eps, s)) != FN_OK) return st;
+  int parts = 0;
+  for (int64_t v0 = 0; v0 < V; v0 += c.piece) {
+    const int64_t width = std::min(c.piece, V - v0);
+    const uint16_t* W = static_cast<const uint16_t*>(Wstar) + v0 * d;
+    CUtensorMap ta, tb;
+    // the logits again, and P from them
+    fn::PairGemmParams p;
+    plan_pair_gemm(&p, M, c.piece, (d + 63) / 64, sms, 32, 1);
+    p.N = static_cast<int>(width);
+    p.num_n_tiles = static_cast<int>((width + p.bn - 1) / p.bn);
+    fn::CeGradParams ge;
+    ge.rstd = rstd;
+    ge.lse = static_cast<const float*>(lse);
+    ge.g = static_cast<const float*>(g);
+    ge.targets = static_cast<const long long*>(targets);
+    ge.P = P;
+    ge.cpart = cpart + static_cast<int64_t>(parts) * M;
+    ge.ldp = static_cast<int>(ldp);
+    ge.v0 = static_cast<int>(v0);
+    ge.V = static_cast<int>(V);
+    ge.ignore = ignore_index;
+    parts += 2 * p.num_n_tiles;
+    if ((st = make_k_map(&ta, x, d, M, d, 128)) != FN_OK) return st;
+    if ((st = make_k_map(&tb, W, d, width, d, p.bn / 2)) != FN_OK) return st;
+    if ((st = launch_pair_gemm<fn::PG_BF16, false, false, fn::CeGradEpi>(ta, tb, p, ge, sms, dev, s, "cross entropy P")) != FN_OK)
+      return st;
+    // dx += P W*
+    plan_pair_gemm(&p, M, d, (width + 63) / 64, sms, 32, 1);
+    p.ksplit = c.ksplit;
+    const fn::CeDxParams xe = {acc, static_cast<int>(d), v0 > 0};
+    if ((st = make_k_map(&ta, P, width, M, ldp, 128)) != FN_OK) return st;
+    if ((st = make_mn_map(&tb, W, d, width, d)) != FN_OK) return st;
+    if ((st = launch_pair_gemm<fn::PG_BF16, false, true, fn::CeDxEpi>(ta, tb, p, xe, sms, dev, s, "cross entropy dx")) != FN_OK)
+      return st;
+    // dW* = P^T x
+    plan_pair_gemm(&p, width, d, (M + 63) / 64, sms, 32, 1);
+    const fn::CeDwParams we = {static_cast<uint16_t*>(dWstar) + v0 * d, static_cast<int>(d)};
+    if ((st = make_mn_map(&ta, P, width, M, ldp)) != FN_OK) return st;
+    if ((st = make_mn_map(&tb, x, d, M, d)) != FN_OK) return st;
+    if ((st = launch_pair_gemm<fn::PG_BF16, true, true, fn::CeDwEpi>(ta, tb, p, we, sms, dev, s, "cross entropy dW")) != FN_OK)
+      return st;
+  }
+  cudaError_t e = launch_kernel(fn::k_ce_dx, dim3(static_cast<unsigned>(M)), dim3(256), 0, s, 1, static_cast<const float*>(acc),
+                                static_cast<const float*>(cpart), static_cast<const float*>(rstd),
+                                static_cast<const uint16_t*>(x), static_cast<const long long*>(targets),
+                                static_cast<uint16_t*>(dx), static_cast<int>(M), static_cast<int>(d), static_cast<int>(V),
+                                c.ksplit, parts, static_cast<long long>(ignore_index));
+  return e == cudaSuccess ? FN_OK : cuda_fail(e, "cross entropy dx launch");
+}
+
+}  // extern "C"

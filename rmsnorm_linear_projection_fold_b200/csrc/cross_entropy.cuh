@@ -1,0 +1,344 @@
+// cross_entropy.cuh — softmax cross entropy of the vocabulary head behind the final RMSNorm, and its gradient, without
+// keeping the logits.
+//
+// The head is one more projection behind a norm, so the gain is folded into it and 1/rms deferred ("FlashNorm: Fast
+// Normalization for Transformers", Abstract): with r[m] = 1/sqrt(mean(x[m]^2) + eps),
+//     l[m, n] = r[m] sum_k x[m, k] W*[n, k],   lse[m] = log sum_n exp(l[m, n]),   loss[m] = lse[m] - l[m, t[m]].
+// Forward: the logits of a 256-row tile exist only in tensor memory; each epilogue thread owns a row and keeps the
+// running maximum and sum of exponentials of its columns, one (max, sum) pair per row, column tile and warp half goes
+// to the workspace, and a second kernel joins them in a fixed order.
+// Backward, in pieces of the vocabulary: the logits are computed again and leave the chip as the factor both gradients
+// share, P[m, n] = r[m] dl[m, n] in bf16, dl[m, n] = g[m] (exp(l - lse) - [n = t]):
+//     dW*[n, :] = sum_m P[m, n] x[m, :]
+//     dx[m, :]  = sum_n P[m, n] W*[n, :] - x[m, :] (r[m]^2 / d) c[m],   c[m] = sum_n dl[m, n] l[m, n]
+// (the second term is the norm's own share: dr/dx = -r^3 x / d). Rounding P to bf16, half a step of 2^-8 per element
+// against tensor-core speed in both products, is the one narrow rounding before the outputs'; their sums, c and the
+// statistics are fp32.
+#pragma once
+
+#include "elementwise.cuh"
+#include "pair_gemm.cuh"
+
+namespace fn {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float v) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v));
+  return e;
+}
+
+// r[m] = 1/sqrt(mean(x[m]^2) + eps), one warp per row.
+__global__ void __launch_bounds__(256) k_row_rstd(const uint16_t* __restrict__ x, float* __restrict__ rstd, int M, int K,
+                                                  float eps) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (row >= M) return;
+  const uint4* src = reinterpret_cast<const uint4*>(x + static_cast<size_t>(row) * K);
+  float s0 = 0.f, s1 = 0.f;
+#pragma unroll 4
+  for (int c = lane; c < (K >> 3); c += 32) {
+    const uint4 v = src[c];
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float a = bf16lo_to_f32(w[e]), b = bf16hi_to_f32(w[e]);
+      s0 = fmaf(a, a, s0);
+      s1 = fmaf(b, b, s1);
+    }
+  }
+  const float ss = warp_sum(s0 + s1);
+  if (lane == 0) rstd[row] = 1.0f / sqrtf(ss / static_cast<float>(K) + eps);
+}
+
+// What a target says: a class, nothing (ignore_index), or neither (reported to the host).
+__device__ __forceinline__ bool target_is_class(long long t, int V) { return t >= 0 && t < V; }
+
+// ---------------------------------------------------------------------------------------------- forward
+
+struct CeFwdParams {
+  const float* rstd;
+  const long long* targets;
+  float2* part;   // [2 column tiles][M]: running maximum (of log2 e times the logits) and sum of 2^(. - max)
+  float* tlogit;  // [M] logit of the target
+};
+
+struct CeFwdEpi {
+  using Params = CeFwdParams;
+  float r2;       // r log2(e): the exponentials are powers of two
+  long long tgt;
+  __device__ __forceinline__ CeFwdEpi(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
+    const int row = t.row0 + lane;
+    r2 = row < p.M ? __ldcg(e.rstd + row) * kLog2e : 0.f;
+    tgt = row < p.M ? __ldg(e.targets + row) : -1;
+  }
+  __device__ __forceinline__ void run(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
+    const int row = t.row0 + lane;
+    float m = -INFINITY, s = 0.f;
+    for (int ch = (t.half + t.turn) & 1; ch * 32 < t.width; ch += 2) {
+      const int c0 = ch * 32;
+      uint32_t v[2][16];
+      tmem_ld16(t.t_row + c0, v[0]);
+      tmem_ld16(t.t_row + c0 + 16, v[1]);
+      tmem_ld_wait();
+      reg_fence16(v[0]);
+      reg_fence16(v[1]);
+      float l[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) l[j] = __uint_as_float(v[j >> 4][j & 15]) * r2;
+      if (c0 + 32 > t.width) {  // columns past the vocabulary take no part
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (c0 + j >= t.width) l[j] = -INFINITY;
+      }
+      const long long at = tgt - (t.n0 + c0);
+      if (at >= 0 && at < 32) {
+        float lt = 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (at == j) lt = __uint_as_float(v[j >> 4][j & 15]);
+        if (c0 + at < t.width) e.tlogit[row] = lt * __ldcg(e.rstd + row);
+      }
+      float mc = l[0];
+#pragma unroll
+      for (int j = 1; j < 32; ++j) mc = fmaxf(mc, l[j]);
+      const float mn = fmaxf(m, mc);
+      const float base = mn == -INFINITY ? 0.f : mn;  // a row of -inf so far: 2^(-inf) = 0, not NaN
+      float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        a0 += ex2(l[j] - base);
+        a1 += ex2(l[j + 1] - base);
+      }
+      s = s * ex2(m - base) + (a0 + a1);
+      m = mn;
+    }
+    if (row < p.M) e.part[static_cast<size_t>(2 * t.nt + t.half) * p.M + row] = make_float2(m, s);
+  }
+};
+
+// lse and loss of 32 rows per block: eight warps take the partial pairs in turn (a fixed order), then one joins the
+// eight. An ignored row's loss is 0; a target that is neither a class nor ignore_index gives NaN and is reported.
+__global__ void __launch_bounds__(256) k_ce_join(const float2* __restrict__ part, const float* __restrict__ tlogit,
+                                                 const long long* __restrict__ targets, float* __restrict__ loss,
+                                                 float* __restrict__ lse, int M, int V, int parts, long long ignore) {
+  __shared__ float2 red[8][32];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int row = blockIdx.x * 32 + lane;
+  float m = -INFINITY, s = 0.f;
+  auto join = [&](float2 q) {
+    const float mn = fmaxf(m, q.x);
+    const float base = mn == -INFINITY ? 0.f : mn;
+    s = s * ex2(m - base) + q.y * ex2(q.x - base);
+    m = mn;
+  };
+  if (row < M) {
+#pragma unroll 4
+    for (int i = w; i < parts; i += 8) join(__ldcg(part + static_cast<size_t>(i) * M + row));
+  }
+  red[w][lane] = make_float2(m, s);
+  __syncthreads();
+  if (w == 0 && row < M) {
+    for (int i = 1; i < 8; ++i) join(red[i][lane]);
+    const float z = m * kLn2 + logf(s);
+    const long long t = targets[row];
+    lse[row] = z;
+    if (t == ignore) {
+      loss[row] = 0.f;
+    } else if (target_is_class(t, V)) {
+      loss[row] = z - __ldcg(tlogit + row);
+    } else {
+      loss[row] = __int_as_float(0x7fc00000);
+      atomicOr(&g_device_status, kStatusBadTarget);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------------------- backward
+
+struct CeGradParams {
+  const float* rstd;
+  const float* lse;
+  const float* g;  // dL/dloss per row
+  const long long* targets;
+  uint16_t* P;     // bf16 [M][ldp], this piece's columns
+  float* cpart;    // [2 column tiles][M] partial c, this piece's
+  int ldp;         // a multiple of 8
+  int v0;          // first column of the piece within the vocabulary
+  int V;           // classes
+  long long ignore;
+};
+
+struct CeGradEpi {
+  using Params = CeGradParams;
+  float r, nlse2, g;  // nlse2 = -lse log2(e)
+  long long tgt;      // relative to the piece
+  __device__ __forceinline__ CeGradEpi(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
+    const int row = t.row0 + lane;
+    r = g = nlse2 = 0.f;
+    tgt = -1;
+    if (row < p.M) {
+      const long long c = __ldg(e.targets + row);
+      // rows without a class (ignored, or reported by the last kernel) have no gradient, whatever they hold
+      if (c != e.ignore && target_is_class(c, e.V)) {
+        g = __ldg(e.g + row);
+        r = __ldcg(e.rstd + row);
+        nlse2 = -__ldg(e.lse + row) * kLog2e;
+        tgt = c - e.v0;
+      } else {
+        tgt = INT64_MIN;
+      }
+    }
+  }
+  __device__ __forceinline__ void run(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
+    const int row = t.row0 + lane;
+    const bool none = tgt == INT64_MIN;
+    const float r2 = r * kLog2e;
+    float c = 0.f;
+    for (int ch = (t.half + t.turn) & 1; ch * 32 < t.width; ch += 2) {
+      const int c0 = ch * 32;
+      uint32_t v[2][16];
+      tmem_ld16(t.t_row + c0, v[0]);
+      tmem_ld16(t.t_row + c0 + 16, v[1]);
+      tmem_ld_wait();
+      reg_fence16(v[0]);
+      reg_fence16(v[1]);
+      const long long at = tgt - (t.n0 + c0);
+      float o[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const float z = __uint_as_float(v[j >> 4][j & 15]);
+        float q = ex2(fmaf(z, r2, nlse2));
+        if (at == j) q -= 1.0f;
+        q *= g;
+        if (none || c0 + j >= t.width) q = 0.f;  // also keeps what a dead row holds (infinities, NaN) out
+        c = fmaf(q, none ? 0.f : z, c);
+        o[j] = q * r;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        pg_put(t.stage, lane, j, make_uint4(pack_bf16x2(o[8 * j], o[8 * j + 1]), pack_bf16x2(o[8 * j + 2], o[8 * j + 3]),
+                                            pack_bf16x2(o[8 * j + 4], o[8 * j + 5]), pack_bf16x2(o[8 * j + 6], o[8 * j + 7])));
+      pg_flush(t.stage, lane, e.P, static_cast<size_t>(e.ldp) * 2, t.row0, p.M, 2ll * (t.n0 + c0), 2ll * e.ldp);
+    }
+    if (row < p.M) e.cpart[static_cast<size_t>(2 * t.nt + t.half) * p.M + row] = c * r;
+  }
+};
+
+// dW*: the product as it is, rounded to bf16 once.
+struct CeDwParams {
+  uint16_t* y;
+  int ldy;
+};
+struct CeDwEpi {
+  using Params = CeDwParams;
+  __device__ __forceinline__ CeDwEpi(const Params&, const PairGemmParams&, const PgTile&, int) {}
+  __device__ __forceinline__ void run(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
+    for (int ch = (t.half + t.turn) & 1; ch * 32 < t.width; ch += 2) {
+      uint32_t v[2][16];
+      tmem_ld16(t.t_row + ch * 32, v[0]);
+      tmem_ld16(t.t_row + ch * 32 + 16, v[1]);
+      tmem_ld_wait();
+      reg_fence16(v[0]);
+      reg_fence16(v[1]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t* w = &v[j >> 1][8 * (j & 1)];
+        pg_put(t.stage, lane, j,
+               make_uint4(pack_bf16x2(__uint_as_float(w[0]), __uint_as_float(w[1])),
+                          pack_bf16x2(__uint_as_float(w[2]), __uint_as_float(w[3])),
+                          pack_bf16x2(__uint_as_float(w[4]), __uint_as_float(w[5])),
+                          pack_bf16x2(__uint_as_float(w[6]), __uint_as_float(w[7]))));
+      }
+      pg_flush(t.stage, lane, e.y, static_cast<size_t>(e.ldy) * 2, t.row0, p.M, 2ll * (t.n0 + ch * 32), 2ll * e.ldy);
+    }
+  }
+};
+
+// dx: fp32 sums over the pieces of the vocabulary, one plane per K range; the first piece writes, later ones add.
+struct CeDxParams {
+  float* acc;  // [K ranges][M][ld]
+  int ld;      // a multiple of 8
+  int add;
+};
+struct CeDxEpi {
+  using Params = CeDxParams;
+  __device__ __forceinline__ CeDxEpi(const Params&, const PairGemmParams&, const PgTile&, int) {}
+  __device__ __forceinline__ void run(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
+    float* plane = e.acc + static_cast<size_t>(t.kz) * p.M * e.ld;
+    for (int ch = (t.half + t.turn) & 1; ch * 16 < t.width; ch += 2) {
+      uint32_t v[16];
+      tmem_ld16(t.t_row + ch * 16, v);
+      tmem_ld_wait();
+      reg_fence16(v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) pg_put(t.stage, lane, j, make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+      __syncwarp();
+      const int seg = lane & 3, col = t.n0 + ch * 16 + 4 * seg;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int rr = 8 * i + (lane >> 2), row = t.row0 + rr;
+        float4 s = *reinterpret_cast<const float4*>(t.stage + rr * 64 + (((seg ^ (rr >> 1)) & 3) << 4));
+        if (row < p.M && col < e.ld) {
+          float4* dst = reinterpret_cast<float4*>(plane + static_cast<size_t>(row) * e.ld + col);
+          if (e.add) {
+            const float4 old = __ldcg(dst);
+            s = make_float4(s.x + old.x, s.y + old.y, s.z + old.z, s.w + old.w);
+          }
+          __stcg(dst, s);
+        }
+      }
+      __syncwarp();
+    }
+  }
+};
+
+// dx[m, :] = sum of the planes - x[m, :] (r^2 / d) c[m], one block per row; c is the partial sums in a fixed order.
+__global__ void __launch_bounds__(256) k_ce_dx(const float* __restrict__ acc, const float* __restrict__ cpart,
+                                               const float* __restrict__ rstd, const uint16_t* __restrict__ x,
+                                               const long long* __restrict__ targets, uint16_t* __restrict__ dx, int M,
+                                               int K, int V, int planes, int parts, long long ignore) {
+  __shared__ float red[8];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int row = blockIdx.x;
+  const long long t = targets[row];
+  uint4* dst = reinterpret_cast<uint4*>(dx + static_cast<size_t>(row) * K);
+  if (t == ignore || !target_is_class(t, V)) {
+    const bool bad = t != ignore;
+    const uint32_t w = bad ? 0x7FC07FC0u : 0u;
+    for (int c = threadIdx.x; c < (K >> 3); c += 256) dst[c] = make_uint4(w, w, w, w);
+    if (bad && threadIdx.x == 0) atomicOr(&g_device_status, kStatusBadTarget);
+    return;
+  }
+  float c = 0.f;
+  for (int i = threadIdx.x; i < parts; i += 256) c += __ldcg(cpart + static_cast<size_t>(i) * M + row);
+  c = warp_sum(c);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = c;
+  __syncthreads();
+  c = ((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7]));
+  const float r = rstd[row];
+  const float k = r * r / static_cast<float>(K) * c;
+  const uint4* xr = reinterpret_cast<const uint4*>(x + static_cast<size_t>(row) * K);
+  for (int i = threadIdx.x; i < (K >> 3); i += 256) {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    for (int z = 0; z < planes; ++z) {
+      const float4* src = reinterpret_cast<const float4*>(acc + (static_cast<size_t>(z) * M + row) * K) + 2 * i;
+      const float4 p = __ldcg(src), q = __ldcg(src + 1);
+      a = make_float4(a.x + p.x, a.y + p.y, a.z + p.z, a.w + p.w);
+      b = make_float4(b.x + q.x, b.y + q.y, b.z + q.z, b.w + q.w);
+    }
+    const uint4 v = xr[i];
+    dst[i] = make_uint4(pack_bf16x2(fmaf(-k, bf16lo_to_f32(v.x), a.x), fmaf(-k, bf16hi_to_f32(v.x), a.y)),
+                        pack_bf16x2(fmaf(-k, bf16lo_to_f32(v.y), a.z), fmaf(-k, bf16hi_to_f32(v.y), a.w)),
+                        pack_bf16x2(fmaf(-k, bf16lo_to_f32(v.z), b.x), fmaf(-k, bf16hi_to_f32(v.z), b.y)),
+                        pack_bf16x2(fmaf(-k, bf16lo_to_f32(v.w), b.z), fmaf(-k, bf16hi_to_f32(v.w), b.w)));
+  }
+}
+
+}  // namespace fn

@@ -26,6 +26,7 @@
 #include "postnorm_pair.cuh"
 #include "postnorm_split.cuh"
 #include "rope.cuh"
+#include "cross_entropy.cuh"
 
 namespace {
 
@@ -1412,6 +1413,8 @@ fn_status flashnorm_check_device_error(void* stream) {
     if (h & fn::kStatusTimeout) return fail(FN_ERR_TIMEOUT, "a kernel gave up on a bounded wait");
     if (h & fn::kStatusBadPosition)
       return fail(FN_ERR_INVALID_ARG, "a RoPE position was outside [0, max_pos); those rows were written as NaN");
+    if (h & fn::kStatusBadTarget)
+      return fail(FN_ERR_INVALID_ARG, "a cross entropy target was neither a class nor ignore_index; its row was written as NaN");
   }
   return FN_OK;
 }
@@ -1448,3 +1451,4 @@ int flashnorm_version(void) { return 100; }
 #include "api_pair_gemm.cuh"
 #include "api_int8.cuh"
 #include "api_rope.cuh"
+#include "api_cross_entropy.cuh"

@@ -14,6 +14,7 @@ namespace fn {
 __device__ unsigned int g_device_status;
 constexpr unsigned int kStatusTimeout = 1u;
 constexpr unsigned int kStatusBadPosition = 2u;  // a RoPE position outside its table (row written as NaN)
+constexpr unsigned int kStatusBadTarget = 4u;    // a cross entropy target that is neither a class nor ignored
 
 // A wait that has not completed after this long is treated as a hang: the kernel records the
 // timeout and returns. Real waits in these kernels last microseconds. Expiry needs BOTH the global

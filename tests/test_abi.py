@@ -399,3 +399,28 @@ def test_int8_validation(lib):
     for shape in [(4, 584, 960, 0), (4, 576, 964, 0), (-1, 576, 960, 0), (4, 576, 24, 1), (4, 576, 960, 3)]:
         assert size(*shape, out) == fn.FN_ERR_INVALID_ARG, shape
     assert size(0, 576, 960, 0, out) == fn.FN_OK and n.value == 0
+
+
+def test_cross_entropy_validation(lib):
+    fwd, bwd = lib.flashnorm_linear_cross_entropy, lib.flashnorm_linear_cross_entropy_backward
+    size = lib.flashnorm_cross_entropy_workspace_bytes
+    big = 1 << 40
+    for M, d, V in [(-1, 64, 100), (4, 60, 100), (4, 0, 100), (4, 64, 0), (4, 64, 1 << 31)]:
+        assert fwd(P, P, P, P, P, M, d, V, 1e-6, -100, P, big, NULL) == fn.FN_ERR_INVALID_ARG
+        assert bwd(P, P, P, P, P, P, P, M, d, V, 1e-6, -100, P, big, NULL) == fn.FN_ERR_INVALID_ARG
+    assert fwd(P, P, P, P, P, 4, 64, 100, -1.0, -100, P, big, NULL) == fn.FN_ERR_INVALID_ARG
+    assert fwd(P, P, P, P, P, 4, 64, 100, 1e-6, -100, P, -1, NULL) == fn.FN_ERR_INVALID_ARG
+    assert fwd(P, P, P, P, P, 4, 64, 100, 1e-6, -100, NULL, 0, NULL) == fn.FN_ERR_INVALID_ARG
+    for i in range(5):
+        for p, want in ((NULL, fn.FN_ERR_INVALID_ARG), (P_MISALIGNED, fn.FN_ERR_ALIGN)):
+            assert fwd(*[p if j == i else P for j in range(5)], 4, 64, 100, 1e-6, -100, P, big, NULL) == want
+    for i in range(7):
+        for p, want in ((NULL, fn.FN_ERR_INVALID_ARG), (P_MISALIGNED, fn.FN_ERR_ALIGN)):
+            assert bwd(*[p if j == i else P for j in range(7)], 4, 64, 100, 1e-6, -100, P, big, NULL) == want
+    assert fwd(P, P, P, P, P, 0, 64, 100, 1e-6, -100, NULL, 0, NULL) == fn.FN_OK
+    n = ctypes.c_int64(-7)
+    out = ctypes.c_void_p(ctypes.addressof(n))
+    assert size(4, 64, 100, 0, NULL) == fn.FN_ERR_INVALID_ARG
+    assert size(4, 64, 100, 2, out) == fn.FN_ERR_INVALID_ARG
+    assert size(4, 60, 100, 0, out) == fn.FN_ERR_INVALID_ARG
+    assert size(0, 64, 100, 1, out) == fn.FN_OK and n.value == 0
