@@ -34,7 +34,8 @@ struct CePlan {
   int64_t pieces;
   int n_tiles;     // column tiles of a full piece
   int ksplit;      // K ranges of dx's product
-  int64_t rstd, part, tlogit, P, acc, bytes;
+  int64_t rstd, part, tlogit;                        // forward
+  int64_t n_live, rows, rank_of, xc, P, acc, bytes;  // backward (and part)
 };
 
 constexpr int64_t kCePieceBytes = int64_t{64} << 20;  // of P, per piece
@@ -51,9 +52,9 @@ CePlan ce_plan(int64_t M, int64_t d, int64_t V, bool backward, int sms) {
   fn::PairGemmParams g;
   plan_pair_gemm(&g, M, c.piece, (d + 63) / 64, sms, 32, 1);
   c.n_tiles = g.num_n_tiles;
-  c.rstd = 0;
-  c.part = round_up(4 * M, 256);
   if (!backward) {
+    c.rstd = 0;
+    c.part = round_up(4 * M, 256);
     c.tlogit = c.part + round_up(16ll * c.n_tiles * M, 256);
     c.bytes = c.tlogit + round_up(4 * M, 256);
     return c;
@@ -62,14 +63,20 @@ CePlan ce_plan(int64_t M, int64_t d, int64_t V, bool backward, int sms) {
   plan_pair_gemm(&g, M, d, num_kb, sms, 32, 1);
   const int64_t tiles = static_cast<int64_t>(g.num_m_tiles) * g.num_n_tiles;
   c.ksplit = static_cast<int>(std::max<int64_t>(1, std::min(sms / 2 / tiles, num_kb / 8)));
-  c.P = c.part + round_up(8ll * c.n_tiles * c.pieces * M, 256);
-  c.acc = c.P + round_up(2 * M * round_up(c.piece, 8), 256);
+  const int64_t Mp = round_up(M, 64);  // the packed rows, zeros at their end
+  c.n_live = 0;
+  c.rows = 256;
+  c.rank_of = c.rows + round_up(16 * M, 256);
+  c.part = c.rank_of + round_up(4 * M, 256);
+  c.xc = c.part + round_up(8ll * c.n_tiles * c.pieces * M, 256);
+  c.P = c.xc + round_up(2 * Mp * d, 256);
+  c.acc = c.P + 2 * Mp * round_up(c.piece, 64);
   c.bytes = c.acc + 4 * c.ksplit * M * d;
   return c;
 }
 
 fn_status check_ce_shape(int64_t M, int64_t d, int64_t V) {
-  if (M < 0 || M > kMaxDim) return fail(FN_ERR_INVALID_ARG, "M = %lld out of range", (long long)M);
+  if (M < 0 || M > kMaxDim / 2) return fail(FN_ERR_INVALID_ARG, "M = %lld out of range", (long long)M);
   if (d < 8 || d > kMaxDim || d % 8 != 0) return fail(FN_ERR_INVALID_ARG, "d = %lld must be a positive multiple of 8", (long long)d);
   if (V < 1 || V > kMaxDim / 2) return fail(FN_ERR_INVALID_ARG, "V = %lld out of range", (long long)V);
   return FN_OK;
@@ -135,13 +142,14 @@ fn_status flashnorm_linear_cross_entropy(const void* x, const void* Wstar, const
   ep.tlogit = reinterpret_cast<float*>(base + c.tlogit);
   fn::PairGemmParams p;
   plan_pair_gemm(&p, M, V, (d + 63) / 64, sms, 32, 1);
+  p.early = fn::PG_EARLY_AB;  // neither operand depends on the row statistics
   CUtensorMap tx, tw;
   if ((st = make_k_map(&tx, x, d, M, d, 128)) != FN_OK) return st;
   if ((st = make_k_map(&tw, Wstar, d, V, d, p.bn / 2)) != FN_OK) return st;
   if ((st = launch_rstd(x, rstd, M, d, eps, s)) != FN_OK) return st;
   if ((st = launch_pair_gemm<fn::PG_BF16, false, false, fn::CeFwdEpi>(tx, tw, p, ep, sms, dev, s, "cross entropy GEMM")) != FN_OK)
     return st;
-  cudaError_t e = launch_kernel(fn::k_ce_join, dim3(static_cast<unsigned>((M + 31) / 32)), dim3(256), 0, s, 1,
+  cudaError_t e = launch_kernel(fn::k_ce_join, dim3(static_cast<unsigned>((M + 7) / 8)), dim3(256), 0, s, 1,
                                 static_cast<const float2*>(ep.part), static_cast<const float*>(ep.tlogit), ep.targets,
                                 static_cast<float*>(loss), static_cast<float*>(lse), p.M, p.N, 2 * p.num_n_tiles,
                                 static_cast<long long>(ignore_index));
@@ -171,12 +179,22 @@ fn_status flashnorm_linear_cross_entropy_backward(const void* g, const void* x, 
   if (workspace_bytes < c.bytes)
     return fail(FN_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes, (long long)c.bytes);
   uint8_t* base = static_cast<uint8_t*>(workspace);
-  float* rstd = reinterpret_cast<float*>(base + c.rstd);
+  int* n_live = reinterpret_cast<int*>(base + c.n_live);
+  fn::CeRow* rows = reinterpret_cast<fn::CeRow*>(base + c.rows);
+  int* rank_of = reinterpret_cast<int*>(base + c.rank_of);
+  uint16_t* xc = reinterpret_cast<uint16_t*>(base + c.xc);
   float* cpart = reinterpret_cast<float*>(base + c.part);
   uint16_t* P = reinterpret_cast<uint16_t*>(base + c.P);
   float* acc = reinterpret_cast<float*>(base + c.acc);
-  const int64_t ldp = round_up(c.piece, 8);
-  if ((st = launch_rstd(x, rstd, M, d, eps, s)) != FN_OK) return st;
+  const int64_t ldp = round_up(c.piece, 64), Mp = round_up(M, 64);
+  // about 256 blocks at most: each counts the live rows before its own
+  const int64_t per_block = round_up((M + 255) / 256, 8);
+  cudaError_t e = launch_kernel(fn::k_ce_pack, dim3(static_cast<unsigned>((M + per_block - 1) / per_block)), dim3(256), 0, s, 1,
+                                static_cast<const uint16_t*>(x), static_cast<const long long*>(targets),
+                                static_cast<const float*>(lse), static_cast<const float*>(g), xc, rows, rank_of, n_live,
+                                static_cast<int>(M), static_cast<int>(d), static_cast<int>(V),
+                                static_cast<int>(per_block), eps, static_cast<long long>(ignore_index));
+  if (e != cudaSuccess) return cuda_fail(e, "cross entropy pack launch");
   int parts = 0;
   for (int64_t v0 = 0; v0 < V; v0 += c.piece) {
     const int64_t width = std::min(c.piece, V - v0);
@@ -188,42 +206,40 @@ fn_status flashnorm_linear_cross_entropy_backward(const void* g, const void* x, 
     p.N = static_cast<int>(width);
     p.num_n_tiles = static_cast<int>((width + p.bn - 1) / p.bn);
     fn::CeGradParams ge;
-    ge.rstd = rstd;
-    ge.lse = static_cast<const float*>(lse);
-    ge.g = static_cast<const float*>(g);
-    ge.targets = static_cast<const long long*>(targets);
+    ge.rows = rows;
     ge.P = P;
     ge.cpart = cpart + static_cast<int64_t>(parts) * M;
     ge.ldp = static_cast<int>(ldp);
     ge.v0 = static_cast<int>(v0);
-    ge.V = static_cast<int>(V);
-    ge.ignore = ignore_index;
     parts += 2 * p.num_n_tiles;
-    if ((st = make_k_map(&ta, x, d, M, d, 128)) != FN_OK) return st;
+    p.live = n_live;
+    if ((st = make_k_map(&ta, xc, d, Mp, d, 128)) != FN_OK) return st;
     if ((st = make_k_map(&tb, W, d, width, d, p.bn / 2)) != FN_OK) return st;
     if ((st = launch_pair_gemm<fn::PG_BF16, false, false, fn::CeGradEpi>(ta, tb, p, ge, sms, dev, s, "cross entropy P")) != FN_OK)
       return st;
     // dx += P W*
     plan_pair_gemm(&p, M, d, (width + 63) / 64, sms, 32, 1);
     p.ksplit = c.ksplit;
+    p.live = n_live;
     const fn::CeDxParams xe = {acc, static_cast<int>(d), v0 > 0};
-    if ((st = make_k_map(&ta, P, width, M, ldp, 128)) != FN_OK) return st;
+    if ((st = make_k_map(&ta, P, width, Mp, ldp, 128)) != FN_OK) return st;
     if ((st = make_mn_map(&tb, W, d, width, d)) != FN_OK) return st;
     if ((st = launch_pair_gemm<fn::PG_BF16, false, true, fn::CeDxEpi>(ta, tb, p, xe, sms, dev, s, "cross entropy dx")) != FN_OK)
       return st;
     // dW* = P^T x
     plan_pair_gemm(&p, width, d, (M + 63) / 64, sms, 32, 1);
+    p.live = n_live;
+    p.live_is_k = 1;
     const fn::CeDwParams we = {static_cast<uint16_t*>(dWstar) + v0 * d, static_cast<int>(d)};
-    if ((st = make_mn_map(&ta, P, width, M, ldp)) != FN_OK) return st;
-    if ((st = make_mn_map(&tb, x, d, M, d)) != FN_OK) return st;
+    if ((st = make_mn_map(&ta, P, width, Mp, ldp)) != FN_OK) return st;
+    if ((st = make_mn_map(&tb, xc, d, Mp, d)) != FN_OK) return st;
     if ((st = launch_pair_gemm<fn::PG_BF16, true, true, fn::CeDwEpi>(ta, tb, p, we, sms, dev, s, "cross entropy dW")) != FN_OK)
       return st;
   }
-  cudaError_t e = launch_kernel(fn::k_ce_dx, dim3(static_cast<unsigned>(M)), dim3(256), 0, s, 1, static_cast<const float*>(acc),
-                                static_cast<const float*>(cpart), static_cast<const float*>(rstd),
-                                static_cast<const uint16_t*>(x), static_cast<const long long*>(targets),
-                                static_cast<uint16_t*>(dx), static_cast<int>(M), static_cast<int>(d), static_cast<int>(V),
-                                c.ksplit, parts, static_cast<long long>(ignore_index));
+  e = launch_kernel(fn::k_ce_dx, dim3(static_cast<unsigned>(M)), dim3(256), 0, s, 1, static_cast<const float*>(acc),
+                    static_cast<const float*>(cpart), static_cast<const fn::CeRow*>(rows), static_cast<const uint16_t*>(x),
+                    static_cast<const int*>(rank_of), static_cast<uint16_t*>(dx), static_cast<int>(M), static_cast<int>(d),
+                    c.ksplit, parts);
   return e == cudaSuccess ? FN_OK : cuda_fail(e, "cross entropy dx launch");
 }
 

@@ -122,6 +122,7 @@ fn_status run_int8(const void* x, const void* Q, const void* scales, void* y, in
   const int step = glu ? 64 : 32;  // whole epilogue blocks
   fn::PairGemmParams p;
   plan_pair_gemm(&p, M, n_rows, (d + 127) / 128, sms, step, 1);
+  p.early = fn::PG_EARLY_B;  // Q does not depend on the row pass
   if ((st = make_u8_map(&tx, xq, d, M, 128)) != FN_OK) return st;
   if ((st = make_u8_map(&tw, Q, d, n_rows, p.bn / 2)) != FN_OK) return st;
   fn::Int8EpiParams ep;

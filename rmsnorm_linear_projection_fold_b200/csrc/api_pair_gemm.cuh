@@ -14,6 +14,9 @@ void plan_pair_gemm(fn::PairGemmParams* p, int64_t M, int64_t N, int64_t num_kb,
   p->num_n_tiles = static_cast<int>((N + p->bn - 1) / p->bn);
   p->band = std::min(8, p->num_m_tiles);
   p->ksplit = ksplit;
+  p->early = fn::PG_EARLY_NONE;
+  p->live_is_k = 0;
+  p->live = nullptr;
 }
 
 template <int KIND, bool A_MN, bool B_MN, class Epi>

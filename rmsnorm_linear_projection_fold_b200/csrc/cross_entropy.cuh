@@ -7,7 +7,9 @@
 // Forward: the logits of a 256-row tile exist only in tensor memory; each epilogue thread owns a row and keeps the
 // running maximum and sum of exponentials of its columns, one (max, sum) pair per row, column tile and warp half goes
 // to the workspace, and a second kernel joins them in a fixed order.
-// Backward, in pieces of the vocabulary: the logits are computed again and leave the chip as the factor both gradients
+// Backward: rows without a target have no gradient, so the live rows are packed first and only they go through the three
+// products (a batch half of prompt or padding costs half; what such rows hold cannot reach dW*). Then, in pieces of the
+// vocabulary, the logits are computed again and leave the chip as the factor both gradients
 // share, P[m, n] = r[m] dl[m, n] in bf16, dl[m, n] = g[m] (exp(l - lse) - [n = t]):
 //     dW*[n, :] = sum_m P[m, n] x[m, :]
 //     dx[m, :]  = sum_n P[m, n] W*[n, :] - x[m, :] (r[m]^2 / d) c[m],   c[m] = sum_n dl[m, n] l[m, n]
@@ -62,7 +64,7 @@ __device__ __forceinline__ bool target_is_class(long long t, int V) { return t >
 struct CeFwdParams {
   const float* rstd;
   const long long* targets;
-  float2* part;   // [2 column tiles][M]: running maximum (of log2 e times the logits) and sum of 2^(. - max)
+  float2* part;   // [M][2 column tiles]: running maximum (of log2 e times the logits) and sum of 2^(. - max)
   float* tlogit;  // [M] logit of the target
 };
 
@@ -72,8 +74,8 @@ struct CeFwdEpi {
   long long tgt;
   __device__ __forceinline__ CeFwdEpi(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
     const int row = t.row0 + lane;
-    r2 = row < p.M ? __ldcg(e.rstd + row) * kLog2e : 0.f;
-    tgt = row < p.M ? __ldg(e.targets + row) : -1;
+    r2 = row < t.M ? __ldcg(e.rstd + row) * kLog2e : 0.f;
+    tgt = row < t.M ? __ldg(e.targets + row) : -1;
   }
   __device__ __forceinline__ void run(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
     const int row = t.row0 + lane;
@@ -116,35 +118,35 @@ struct CeFwdEpi {
       s = s * ex2(m - base) + (a0 + a1);
       m = mn;
     }
-    if (row < p.M) e.part[static_cast<size_t>(2 * t.nt + t.half) * p.M + row] = make_float2(m, s);
+    if (row < t.M) e.part[static_cast<size_t>(row) * (2 * p.num_n_tiles) + 2 * t.nt + t.half] = make_float2(m, s);
   }
 };
 
-// lse and loss of 32 rows per block: eight warps take the partial pairs in turn (a fixed order), then one joins the
-// eight. An ignored row's loss is 0; a target that is neither a class nor ignore_index gives NaN and is reported.
+// lse and loss, one warp per row: each lane joins every 32nd partial pair, then the lanes join in a butterfly (a fixed
+// order). An ignored row's loss is 0; a target that is neither a class nor ignore_index gives NaN and is reported.
 __global__ void __launch_bounds__(256) k_ce_join(const float2* __restrict__ part, const float* __restrict__ tlogit,
                                                  const long long* __restrict__ targets, float* __restrict__ loss,
                                                  float* __restrict__ lse, int M, int V, int parts, long long ignore) {
-  __shared__ float2 red[8][32];
   grid_dep_wait();
   grid_dep_launch();
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int row = blockIdx.x * 32 + lane;
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (row >= M) return;
   float m = -INFINITY, s = 0.f;
-  auto join = [&](float2 q) {
-    const float mn = fmaxf(m, q.x);
+  auto join = [&](float qm, float qs) {
+    const float mn = fmaxf(m, qm);
     const float base = mn == -INFINITY ? 0.f : mn;
-    s = s * ex2(m - base) + q.y * ex2(q.x - base);
+    s = s * ex2(m - base) + qs * ex2(qm - base);
     m = mn;
   };
-  if (row < M) {
+  const float2* src = part + static_cast<size_t>(row) * parts;
 #pragma unroll 4
-    for (int i = w; i < parts; i += 8) join(__ldcg(part + static_cast<size_t>(i) * M + row));
+  for (int i = lane; i < parts; i += 32) {
+    const float2 q = __ldcg(src + i);
+    join(q.x, q.y);
   }
-  red[w][lane] = make_float2(m, s);
-  __syncthreads();
-  if (w == 0 && row < M) {
-    for (int i = 1; i < 8; ++i) join(red[i][lane]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) join(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
+  if (lane == 0) {
     const float z = m * kLn2 + logf(s);
     const long long t = targets[row];
     lse[row] = z;
@@ -161,44 +163,112 @@ __global__ void __launch_bounds__(256) k_ce_join(const float2* __restrict__ part
 
 // ---------------------------------------------------------------------------------------------- backward
 
+// What the products need of a live row.
+struct __align__(16) CeRow {
+  float rstd, nlse2, g;  // 1/rms, -lse log2(e), dL/dloss
+  int target;
+};
+
+constexpr int kCeIgnored = -1, kCeBad = -2;  // in place of a row's rank among the live ones
+
+// Packs the live rows in order: xc[rank] = x[m], rows[rank], rank_of[m], and their number. Rows up to the next multiple of
+// 64 are zeroed: dW*'s product runs over whole stages of 64 rows. A block serves rows_per_block rows, a warp an eighth of
+// them in order; each counts the live rows before its own, from the targets.
+__global__ void __launch_bounds__(256) k_ce_pack(const uint16_t* __restrict__ x, const long long* __restrict__ targets,
+                                                 const float* __restrict__ lse, const float* __restrict__ g,
+                                                 uint16_t* __restrict__ xc, CeRow* __restrict__ rows,
+                                                 int* __restrict__ rank_of, int* __restrict__ n_live, int M, int K, int V,
+                                                 int rows_per_block, float eps, long long ignore) {
+  grid_dep_wait();
+  grid_dep_launch();
+  __shared__ int counts[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto live_at = [&](int m) {
+    const long long t = __ldg(targets + m);
+    return t != ignore && target_is_class(t, V);
+  };
+  const int b0 = static_cast<int>(blockIdx.x) * rows_per_block;
+  int n = 0;
+  for (int m = threadIdx.x; m < b0; m += 256) n += live_at(m);
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (lane == 0) counts[warp] = n;
+  __syncthreads();
+  int base = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) base += counts[i];
+  const int per_warp = rows_per_block >> 3, m0 = b0 + warp * per_warp;
+  auto count = [&](int from, int to) {
+    int c = 0;
+    for (int m = from + lane; m < to; m += 32) c += live_at(m);
+    return __reduce_add_sync(0xffffffffu, c);
+  };
+  int rank = base + count(b0, min(m0, M));
+  const int chunks = K >> 3;
+  for (int m = m0; m < min(m0 + per_warp, M); ++m) {
+    const long long t = __ldg(targets + m);
+    const bool live = t != ignore && target_is_class(t, V);
+    if (lane == 0) rank_of[m] = live ? rank : t == ignore ? kCeIgnored : kCeBad;
+    if (!live) continue;
+    const uint4* src = reinterpret_cast<const uint4*>(x + static_cast<size_t>(m) * K);
+    uint4* dst = reinterpret_cast<uint4*>(xc + static_cast<size_t>(rank) * K);
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll 4
+    for (int c = lane; c < chunks; c += 32) {
+      const uint4 v = __ldg(src + c);
+      dst[c] = v;
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float a = bf16lo_to_f32(w[e]), b = bf16hi_to_f32(w[e]);
+        s0 = fmaf(a, a, s0);
+        s1 = fmaf(b, b, s1);
+      }
+    }
+    const float ss = warp_sum(s0 + s1);
+    if (lane == 0) {
+      CeRow r;
+      r.rstd = 1.0f / sqrtf(ss / static_cast<float>(K) + eps);
+      r.nlse2 = -__ldg(lse + m) * kLog2e;
+      r.g = __ldg(g + m);
+      r.target = static_cast<int>(t);
+      rows[rank] = r;
+    }
+    ++rank;
+  }
+  if (blockIdx.x == gridDim.x - 1) {
+    const int live = base + count(b0, M);
+    if (threadIdx.x == 0) *n_live = live;
+    const int end = (live + 63) & ~63;
+    for (int r = live + warp; r < end; r += 8) {
+      uint4* dst = reinterpret_cast<uint4*>(xc + static_cast<size_t>(r) * K);
+      for (int c = lane; c < chunks; c += 32) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+}
+
 struct CeGradParams {
-  const float* rstd;
-  const float* lse;
-  const float* g;  // dL/dloss per row
-  const long long* targets;
-  uint16_t* P;     // bf16 [M][ldp], this piece's columns
+  const CeRow* rows;
+  uint16_t* P;     // bf16 [live rows, and up to the next multiple of 64][ldp], this piece's columns
   float* cpart;    // [2 column tiles][M] partial c, this piece's
-  int ldp;         // a multiple of 8
+  int ldp;         // a multiple of 64: rows of P start on whole 128-byte lines
   int v0;          // first column of the piece within the vocabulary
-  int V;           // classes
-  long long ignore;
 };
 
 struct CeGradEpi {
   using Params = CeGradParams;
-  float r, nlse2, g;  // nlse2 = -lse log2(e)
-  long long tgt;      // relative to the piece
+  CeRow q;
   __device__ __forceinline__ CeGradEpi(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
     const int row = t.row0 + lane;
-    r = g = nlse2 = 0.f;
-    tgt = -1;
-    if (row < p.M) {
-      const long long c = __ldg(e.targets + row);
-      // rows without a class (ignored, or reported by the last kernel) have no gradient, whatever they hold
-      if (c != e.ignore && target_is_class(c, e.V)) {
-        g = __ldg(e.g + row);
-        r = __ldcg(e.rstd + row);
-        nlse2 = -__ldg(e.lse + row) * kLog2e;
-        tgt = c - e.v0;
-      } else {
-        tgt = INT64_MIN;
-      }
+    q.rstd = q.nlse2 = q.g = 0.f;
+    q.target = -1;
+    if (row < t.M) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(e.rows + row));
+      q.rstd = v.x, q.nlse2 = v.y, q.g = v.z, q.target = __float_as_int(v.w);
     }
   }
   __device__ __forceinline__ void run(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
     const int row = t.row0 + lane;
-    const bool none = tgt == INT64_MIN;
-    const float r2 = r * kLog2e;
+    const float r2 = q.rstd * kLog2e;
     float c = 0.f;
     for (int ch = (t.half + t.turn) & 1; ch * 32 < t.width; ch += 2) {
       const int c0 = ch * 32;
@@ -208,25 +278,26 @@ struct CeGradEpi {
       tmem_ld_wait();
       reg_fence16(v[0]);
       reg_fence16(v[1]);
-      const long long at = tgt - (t.n0 + c0);
+      const int at = q.target - (e.v0 + t.n0 + c0);
       float o[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
         const float z = __uint_as_float(v[j >> 4][j & 15]);
-        float q = ex2(fmaf(z, r2, nlse2));
-        if (at == j) q -= 1.0f;
-        q *= g;
-        if (none || c0 + j >= t.width) q = 0.f;  // also keeps what a dead row holds (infinities, NaN) out
-        c = fmaf(q, none ? 0.f : z, c);
-        o[j] = q * r;
+        float dl = ex2(fmaf(z, r2, q.nlse2));
+        if (at == j) dl -= 1.0f;
+        dl *= q.g;
+        if (c0 + j >= t.width || row >= t.M) dl = 0.f;
+        c = fmaf(dl, z, c);
+        o[j] = dl * q.rstd;
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         pg_put(t.stage, lane, j, make_uint4(pack_bf16x2(o[8 * j], o[8 * j + 1]), pack_bf16x2(o[8 * j + 2], o[8 * j + 3]),
                                             pack_bf16x2(o[8 * j + 4], o[8 * j + 5]), pack_bf16x2(o[8 * j + 6], o[8 * j + 7])));
-      pg_flush(t.stage, lane, e.P, static_cast<size_t>(e.ldp) * 2, t.row0, p.M, 2ll * (t.n0 + c0), 2ll * e.ldp);
+      // zeros up to the end of the stage of 64 rows that dW*'s product reads
+      pg_flush(t.stage, lane, e.P, static_cast<size_t>(e.ldp) * 2, t.row0, (t.M + 63) & ~63, 2ll * (t.n0 + c0), 2ll * e.ldp);
     }
-    if (row < p.M) e.cpart[static_cast<size_t>(2 * t.nt + t.half) * p.M + row] = c * r;
+    if (row < t.M) e.cpart[static_cast<size_t>(2 * t.nt + t.half) * p.M + row] = c * q.rstd;
   }
 };
 
@@ -246,6 +317,10 @@ struct CeDwEpi {
       tmem_ld_wait();
       reg_fence16(v[0]);
       reg_fence16(v[1]);
+      if (t.empty) {  // no live rows
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j >> 4][j & 15] = 0u;
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint32_t* w = &v[j >> 1][8 * (j & 1)];
@@ -255,7 +330,7 @@ struct CeDwEpi {
                           pack_bf16x2(__uint_as_float(w[4]), __uint_as_float(w[5])),
                           pack_bf16x2(__uint_as_float(w[6]), __uint_as_float(w[7]))));
       }
-      pg_flush(t.stage, lane, e.y, static_cast<size_t>(e.ldy) * 2, t.row0, p.M, 2ll * (t.n0 + ch * 32), 2ll * e.ldy);
+      pg_flush(t.stage, lane, e.y, static_cast<size_t>(e.ldy) * 2, t.row0, t.M, 2ll * (t.n0 + ch * 32), 2ll * e.ldy);
     }
   }
 };
@@ -284,7 +359,7 @@ struct CeDxEpi {
       for (int i = 0; i < 4; ++i) {
         const int rr = 8 * i + (lane >> 2), row = t.row0 + rr;
         float4 s = *reinterpret_cast<const float4*>(t.stage + rr * 64 + (((seg ^ (rr >> 1)) & 3) << 4));
-        if (row < p.M && col < e.ld) {
+        if (row < t.M && col < e.ld) {
           float4* dst = reinterpret_cast<float4*>(plane + static_cast<size_t>(row) * e.ld + col);
           if (e.add) {
             const float4 old = __ldcg(dst);
@@ -298,37 +373,38 @@ struct CeDxEpi {
   }
 };
 
-// dx[m, :] = sum of the planes - x[m, :] (r^2 / d) c[m], one block per row; c is the partial sums in a fixed order.
+// dx[m, :] = sum of the planes - x[m, :] (r^2 / d) c[m], one block per row; planes and partial sums c by the row's rank among
+// the live ones, in a fixed order.
 __global__ void __launch_bounds__(256) k_ce_dx(const float* __restrict__ acc, const float* __restrict__ cpart,
-                                               const float* __restrict__ rstd, const uint16_t* __restrict__ x,
-                                               const long long* __restrict__ targets, uint16_t* __restrict__ dx, int M,
-                                               int K, int V, int planes, int parts, long long ignore) {
+                                               const CeRow* __restrict__ rows, const uint16_t* __restrict__ x,
+                                               const int* __restrict__ rank_of, uint16_t* __restrict__ dx, int M, int K,
+                                               int planes, int parts) {
   __shared__ float red[8];
   grid_dep_wait();
   grid_dep_launch();
   const int row = blockIdx.x;
-  const long long t = targets[row];
+  const int rank = __ldcg(rank_of + row);
   uint4* dst = reinterpret_cast<uint4*>(dx + static_cast<size_t>(row) * K);
-  if (t == ignore || !target_is_class(t, V)) {
-    const bool bad = t != ignore;
+  if (rank < 0) {
+    const bool bad = rank == kCeBad;
     const uint32_t w = bad ? 0x7FC07FC0u : 0u;
     for (int c = threadIdx.x; c < (K >> 3); c += 256) dst[c] = make_uint4(w, w, w, w);
     if (bad && threadIdx.x == 0) atomicOr(&g_device_status, kStatusBadTarget);
     return;
   }
   float c = 0.f;
-  for (int i = threadIdx.x; i < parts; i += 256) c += __ldcg(cpart + static_cast<size_t>(i) * M + row);
+  for (int i = threadIdx.x; i < parts; i += 256) c += __ldcg(cpart + static_cast<size_t>(i) * M + rank);
   c = warp_sum(c);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = c;
   __syncthreads();
   c = ((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7]));
-  const float r = rstd[row];
+  const float r = __ldcg(&rows[rank].rstd);
   const float k = r * r / static_cast<float>(K) * c;
   const uint4* xr = reinterpret_cast<const uint4*>(x + static_cast<size_t>(row) * K);
   for (int i = threadIdx.x; i < (K >> 3); i += 256) {
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
     for (int z = 0; z < planes; ++z) {
-      const float4* src = reinterpret_cast<const float4*>(acc + (static_cast<size_t>(z) * M + row) * K) + 2 * i;
+      const float4* src = reinterpret_cast<const float4*>(acc + (static_cast<size_t>(z) * M + rank) * K) + 2 * i;
       const float4 p = __ldcg(src), q = __ldcg(src + 1);
       a = make_float4(a.x + p.x, a.y + p.y, a.z + p.z, a.w + p.w);
       b = make_float4(b.x + q.x, b.y + q.y, b.z + q.z, b.w + q.w);

@@ -215,7 +215,7 @@ struct Int8Epi {
   using Params = Int8EpiParams;
   float rho;
   __device__ __forceinline__ Int8Epi(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
-    rho = t.row0 + lane < p.M ? __ldcg(e.rho + t.row0 + lane) : 0.f;
+    rho = t.row0 + lane < t.M ? __ldcg(e.rho + t.row0 + lane) : 0.f;
   }
   __device__ __forceinline__ void run(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
     constexpr int kOut = OUT_F32 ? 16 : 32;      // outputs of a staged block (64 bytes of a row)
@@ -259,7 +259,7 @@ struct Int8Epi {
                                               pack_bf16x2(o[8 * j + 4], o[8 * j + 5]), pack_bf16x2(o[8 * j + 6], o[8 * j + 7])));
       }
       const int oc0 = GLU ? (t.n0 + c0) / 2 : t.n0 + c0;
-      pg_flush(t.stage, lane, e.y, static_cast<size_t>(e.n_out) * kEsz, t.row0, p.M, static_cast<long long>(oc0) * kEsz,
+      pg_flush(t.stage, lane, e.y, static_cast<size_t>(e.n_out) * kEsz, t.row0, t.M, static_cast<long long>(oc0) * kEsz,
                static_cast<long long>(e.n_out) * kEsz);
     }
   }

@@ -37,7 +37,14 @@ struct PairGemmParams {
   int num_n_tiles;
   int band;         // row tiles per band
   int ksplit;       // K ranges; range z of a tile goes to the epilogue as plane z
+  int early;        // PgEarly: operands that do not depend on the previous kernel of the stream
+  int live_is_k;    // what *live counts: rows of C, or (1) k
+  const int* live;  // null, or a count on the device that replaces M (at most M) or num_kb (at most so many stages)
 };
+
+// Operands that may be fetched before the previous kernel has completed. That kernel must itself have waited for all
+// work before it (griddepcontrol.wait) before it let this one start, so that what is fetched early is in place.
+enum PgEarly { PG_EARLY_NONE = 0, PG_EARLY_B = 1, PG_EARLY_AB = 2 };
 
 enum PgKind { PG_BF16 = 0, PG_I8 = 1 };
 
@@ -77,6 +84,8 @@ struct PgTile {
   int half;        // which of the quarter's two warps
   int turn;        // tile counter of this pair: the warps swap chunks from tile to tile
   int nt, kz;      // column tile and K range
+  int M;           // rows of C
+  bool empty;      // no k at all: the accumulator holds nothing and counts as zero
   uint8_t* stage;  // this warp's staging buffer
 };
 
@@ -154,10 +163,21 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   cluster_sync_all();  // both CTAs' barriers exist before either touches the other's
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
-  grid_dep_wait();  // the previous kernel's outputs (our inputs, or buffers we overwrite) are complete
+  // The previous kernel's outputs (our inputs, or buffers we overwrite) are complete. Early operands do not wait for that;
+  // their producer does once it needs the others, the epilogue always does.
+  if (p.early == PG_EARLY_NONE || warp >= 2) grid_dep_wait();
 
+  int rows = p.M, num_kb = p.num_kb;
+  if (p.live != nullptr) {  // never with early operands
+    const int live = __ldcg(p.live);
+    if (p.live_is_k)
+      num_kb = (live + kK - 1) / kK;
+    else
+      rows = live;
+  }
+  const int num_m_tiles = (rows + 255) >> 8;
   const int cl = static_cast<int>(blockIdx.x) >> 1, ncl = static_cast<int>(gridDim.x) >> 1;
-  const int tiles = p.num_m_tiles * p.num_n_tiles;
+  const int tiles = num_m_tiles * p.num_n_tiles;
   const int items = tiles * p.ksplit;
   // Item t: its row and column tile (bands of p.band row tiles, row tile fastest) and K range.
   auto item_at = [&](int t, int& mt, int& nt, int& kz, int& kb0, int& kb1) {
@@ -165,11 +185,11 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     const int u = t - kz * tiles;
     const int per_band = p.band * p.num_n_tiles;
     const int b = u / per_band, r = u - b * per_band;
-    const int rows = min(p.band, p.num_m_tiles - b * p.band);
-    mt = b * p.band + r % rows;
-    nt = r / rows;
-    kb0 = static_cast<int>(static_cast<long long>(kz) * p.num_kb / p.ksplit);
-    kb1 = static_cast<int>(static_cast<long long>(kz + 1) * p.num_kb / p.ksplit);
+    const int in_band = min(p.band, num_m_tiles - b * p.band);
+    mt = b * p.band + r % in_band;
+    nt = r / in_band;
+    kb0 = static_cast<int>(static_cast<long long>(kz) * num_kb / p.ksplit);
+    kb1 = static_cast<int>(static_cast<long long>(kz + 1) * num_kb / p.ksplit);
   };
   const int bh = p.bn / 2;                // B rows per CTA
   const int b_boxes = (bh + 63) / 64;     // MN-major: 64-wide boxes per CTA
@@ -182,30 +202,50 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       bool ok = true;
       const uint32_t stage_bytes =
           static_cast<uint32_t>(kPgTileBytes + (B_MN ? b_boxes * 8192 : bh * 128));
+      auto load_a = [&](int st, int kb, int m0) {
+        const uint32_t bar = dsmem_addr(&full[st], 0);
+        if (A_MN) {
+          tma_load_2d_pair(sA + st * kPgTileBytes, &tm_a, bar, m0, kb * kK);
+          tma_load_2d_pair(sA + st * kPgTileBytes + 8192, &tm_a, bar, m0 + 64, kb * kK);
+        } else {
+          tma_load_2d_pair(sA + st * kPgTileBytes, &tm_a, bar, kb * kK, m0);
+        }
+      };
+      auto load_b = [&](int st, int kb, int n0) {
+        const uint32_t bar = dsmem_addr(&full[st], 0);
+        if (B_MN) {
+          for (int j = 0; j < b_boxes; ++j)
+            tma_load_2d_pair(sB + st * kPgTileBytes + j * 8192, &tm_b, bar, n0 + 64 * j, kb * kK);
+        } else {
+          tma_load_2d_pair(sB + st * kPgTileBytes, &tm_b, bar, kb * kK, n0);
+        }
+      };
+      int ahead = 0;  // stages whose B is already on its way
+      if (p.early == PG_EARLY_B && cl < items) {
+        int mt, nt, kz, kb0, kb1;
+        item_at(cl, mt, nt, kz, kb0, kb1);
+        ahead = min(kPgStages, kb1 - kb0);
+        for (int st = 0; st < ahead; ++st) {  // every stage is free at the start
+          if (leader) mbar_arrive_expect_tx(&full[st], 2 * stage_bytes);
+          load_b(st, kb0 + st, nt * p.bn + static_cast<int>(rank) * bh);
+        }
+      }
+      if (p.early == PG_EARLY_B) grid_dep_wait();
       for (int t = cl; t < items && ok; t += ncl) {
         int mt, nt, kz, kb0, kb1;
         item_at(t, mt, nt, kz, kb0, kb1);
         const int m0 = mt * 256 + static_cast<int>(rank) * 128;
         const int n0 = nt * p.bn + static_cast<int>(rank) * bh;
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait_cluster(&empty[s], ph ^ 1u, abort_flag)) {
-            ok = false;
-            break;
+          if (issued >= ahead) {
+            if (!mbar_wait_cluster(&empty[s], ph ^ 1u, abort_flag)) {
+              ok = false;
+              break;
+            }
+            if (leader) mbar_arrive_expect_tx(&full[s], 2 * stage_bytes);
+            load_b(s, kb, n0);
           }
-          const uint32_t leader_full = dsmem_addr(&full[s], 0);
-          if (leader) mbar_arrive_expect_tx(&full[s], 2 * stage_bytes);
-          if (A_MN) {
-            tma_load_2d_pair(sA + s * kPgTileBytes, &tm_a, leader_full, m0, kb * kK);
-            tma_load_2d_pair(sA + s * kPgTileBytes + 8192, &tm_a, leader_full, m0 + 64, kb * kK);
-          } else {
-            tma_load_2d_pair(sA + s * kPgTileBytes, &tm_a, leader_full, kb * kK, m0);
-          }
-          if (B_MN) {
-            for (int j = 0; j < b_boxes; ++j)
-              tma_load_2d_pair(sB + s * kPgTileBytes + j * 8192, &tm_b, leader_full, n0 + 64 * j, kb * kK);
-          } else {
-            tma_load_2d_pair(sB + s * kPgTileBytes, &tm_b, leader_full, kb * kK, n0);
-          }
+          load_a(s, kb, m0);
           ++issued;
           if (++s == kPgStages) {
             s = 0;
@@ -314,6 +354,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       tile.turn = turn;
       tile.nt = nt;
       tile.kz = kz;
+      tile.M = rows;
+      tile.empty = kb0 == kb1;
       tile.stage = sOut + (warp - 2) * kPgOutBytes;
       tile.t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * 256);
       Epi epi(ep, p, tile, lane);  // row parameters are on their way while the MMAs finish

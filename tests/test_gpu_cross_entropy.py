@@ -149,6 +149,31 @@ def test_gradient_matches_differences():
         assert abs(float((got * v).sum()) - diff) <= float(((tol + HB * got.abs()) * v.abs()).sum()) + 1e-8
 
 
+def test_masked_rows_hold_anything():
+    """Rows without a target (padding) may hold NaN or infinities: the others' losses and all gradients stay what they are
+    without those rows; every row ignored gives zero gradients."""
+    M, d, V = 75, 144, 1003
+    x, W, t, g = _draw(M, d, V, seed=5)
+    t[10:20] = -100
+    keep = t != -100
+    args = [v.cuda() for v in (x, W, t)]
+    loss, lse = fn.flashnorm_linear_cross_entropy(*args, EPS)
+    dx, dW = fn.flashnorm_linear_cross_entropy_backward(g.cuda(), *args, lse, EPS)
+    for value in (float("nan"), float("inf"), -float("inf"), 3e38):
+        xb, gb = x.clone(), g.clone()
+        xb[~keep], gb[~keep] = value, value
+        bad = [v.cuda() for v in (xb, W, t)]
+        lossb, lseb = fn.flashnorm_linear_cross_entropy(*bad, EPS)
+        assert torch.equal(lossb, loss) and torch.equal(lseb[keep.cuda()], lse[keep.cuda()])
+        dxb, dWb = fn.flashnorm_linear_cross_entropy_backward(gb.cuda(), *bad, lseb, EPS)
+        assert torch.equal(dxb, dx) and torch.equal(dWb, dW)
+    t[:] = -100
+    loss, lse = fn.flashnorm_linear_cross_entropy(args[0], args[1], t.cuda(), EPS)
+    dx, dW = fn.flashnorm_linear_cross_entropy_backward(g.cuda(), args[0], args[1], t.cuda(), lse, EPS)
+    assert (loss == 0).all() and (dx == 0).all() and (dW == 0).all() and lse.isfinite().all()
+    fn.flashnorm_check_device_error()
+
+
 def test_ignore_index_may_be_a_class():
     M, d, V = 40, 64, 300
     x, W, t, g = _draw(M, d, V, seed=6, ignore=7)
