@@ -38,6 +38,8 @@ struct CePlan {
   int64_t n_live, rows, rank_of, xc, P, acc, bytes;  // backward (and part)
 };
 
+// Tile widths of the products whose B is MN-major: each CTA's half is whole 64-column boxes, which start on 128-byte lines.
+constexpr int kMnStep = 128;
 constexpr int64_t kCePieceBytes = int64_t{64} << 20;  // of P, per piece
 
 CePlan ce_plan(int64_t M, int64_t d, int64_t V, bool backward, int sms) {
@@ -60,7 +62,7 @@ CePlan ce_plan(int64_t M, int64_t d, int64_t V, bool backward, int sms) {
     return c;
   }
   const int64_t num_kb = (c.piece + 63) / 64;
-  plan_pair_gemm(&g, M, d, num_kb, sms, 32, 1);
+  plan_pair_gemm(&g, M, d, num_kb, sms, kMnStep, 1);
   const int64_t tiles = static_cast<int64_t>(g.num_m_tiles) * g.num_n_tiles;
   c.ksplit = static_cast<int>(std::max<int64_t>(1, std::min(sms / 2 / tiles, num_kb / 8)));
   const int64_t Mp = round_up(M, 64);  // the packed rows, zeros at their end
@@ -218,7 +220,7 @@ fn_status flashnorm_linear_cross_entropy_backward(const void* g, const void* x, 
     if ((st = launch_pair_gemm<fn::PG_BF16, false, false, fn::CeGradEpi>(ta, tb, p, ge, sms, dev, s, "cross entropy P")) != FN_OK)
       return st;
     // dx += P W*
-    plan_pair_gemm(&p, M, d, (width + 63) / 64, sms, 32, 1);
+    plan_pair_gemm(&p, M, d, (width + 63) / 64, sms, kMnStep, 1);
     p.ksplit = c.ksplit;
     p.live = n_live;
     const fn::CeDxParams xe = {acc, static_cast<int>(d), v0 > 0};
@@ -227,7 +229,7 @@ fn_status flashnorm_linear_cross_entropy_backward(const void* g, const void* x, 
     if ((st = launch_pair_gemm<fn::PG_BF16, false, true, fn::CeDxEpi>(ta, tb, p, xe, sms, dev, s, "cross entropy dx")) != FN_OK)
       return st;
     // dW* = P^T x
-    plan_pair_gemm(&p, width, d, (M + 63) / 64, sms, 32, 1);
+    plan_pair_gemm(&p, width, d, (M + 63) / 64, sms, kMnStep, 1);
     p.live = n_live;
     p.live_is_k = 1;
     const fn::CeDwParams we = {static_cast<uint16_t*>(dWstar) + v0 * d, static_cast<int>(d)};
