@@ -35,11 +35,26 @@ struct CePlan {
   int n_tiles;     // column tiles of a full piece
   int ksplit;      // K ranges of dx's product
   int64_t rstd, part, tlogit;                        // forward
-  int64_t n_live, rows, rank_of, xc, P, acc, bytes;  // backward (and part)
+  int64_t n_live, rows, rank_of, target, u, xc, P, acc, bytes;  // backward (and part)
 };
 
-// Tile widths of the products whose B is MN-major: each CTA's half is whole 64-column boxes, which start on 128-byte lines.
-constexpr int kMnStep = 128;
+// Stages per accumulation of the forward's logits: 1024 k keep the drift of the tensor core's sums near 1e-6.
+constexpr int kCeFwdChunk = 16;
+
+// Tile width of the products whose B is MN-major (x or W*, [k][d]).
+int ce_mn_width(int64_t d) { return d > 128 ? 256 : 128; }
+
+// K ranges of dx's product: few enough planes, many enough items that its share of a pair's work fits into an even part
+// of both products'.
+int ce_dx_ksplit(const fn::PairGemmParams& dx, const fn::PairGemmParams& dw, int pairs) {
+  const int64_t items = static_cast<int64_t>(dx.num_m_tiles) * dx.num_n_tiles;
+  const int64_t all = items * dx.num_kb + static_cast<int64_t>(dw.num_m_tiles) * dw.num_n_tiles * dw.num_kb;
+  const int64_t even = (all + pairs - 1) / pairs;
+  int k = 1;
+  while (k < 64 && dx.num_kb / (k + 1) >= 8 && (items * k + pairs - 1) / pairs * ((dx.num_kb + k - 1) / k) > even) ++k;
+  return k;
+}
+
 constexpr int64_t kCePieceBytes = int64_t{64} << 20;  // of P, per piece
 
 CePlan ce_plan(int64_t M, int64_t d, int64_t V, bool backward, int sms) {
@@ -52,7 +67,7 @@ CePlan ce_plan(int64_t M, int64_t d, int64_t V, bool backward, int sms) {
     c.pieces = (V + c.piece - 1) / c.piece;
   }
   fn::PairGemmParams g;
-  plan_pair_gemm(&g, M, c.piece, (d + 63) / 64, sms, 32, 1);
+  plan_pair_gemm(&g, M, c.piece, (d + 63) / 64, sms, 32);
   c.n_tiles = g.num_n_tiles;
   if (!backward) {
     c.rstd = 0;
@@ -61,15 +76,17 @@ CePlan ce_plan(int64_t M, int64_t d, int64_t V, bool backward, int sms) {
     c.bytes = c.tlogit + round_up(4 * M, 256);
     return c;
   }
-  const int64_t num_kb = (c.piece + 63) / 64;
-  plan_pair_gemm(&g, M, d, num_kb, sms, kMnStep, 1);
-  const int64_t tiles = static_cast<int64_t>(g.num_m_tiles) * g.num_n_tiles;
-  c.ksplit = static_cast<int>(std::max<int64_t>(1, std::min(sms / 2 / tiles, num_kb / 8)));
+  fn::PairGemmParams w;
+  plan_pair_gemm_bn(&g, M, d, (c.piece + 63) / 64, ce_mn_width(d), 1);
+  plan_pair_gemm_bn(&w, c.piece, d, (M + 63) / 64, ce_mn_width(d), 1);
+  c.ksplit = ce_dx_ksplit(g, w, sms / 2);
   const int64_t Mp = round_up(M, 64);  // the packed rows, zeros at their end
   c.n_live = 0;
   c.rows = 256;
   c.rank_of = c.rows + round_up(16 * M, 256);
-  c.part = c.rank_of + round_up(4 * M, 256);
+  c.target = c.rank_of + round_up(4 * M, 256);
+  c.u = c.target + round_up(4 * M, 256);
+  c.part = c.u + round_up(4 * M, 256);
   c.xc = c.part + round_up(8ll * c.n_tiles * c.pieces * M, 256);
   c.P = c.xc + round_up(2 * Mp * d, 256);
   c.acc = c.P + 2 * Mp * round_up(c.piece, 64);
@@ -143,14 +160,18 @@ fn_status flashnorm_linear_cross_entropy(const void* x, const void* Wstar, const
   ep.part = reinterpret_cast<float2*>(base + c.part);
   ep.tlogit = reinterpret_cast<float*>(base + c.tlogit);
   fn::PairGemmParams p;
-  plan_pair_gemm(&p, M, V, (d + 63) / 64, sms, 32, 1);
+  plan_pair_gemm(&p, M, V, (d + 63) / 64, sms, 32);
+  p.kchunk = kCeFwdChunk;
   p.early = fn::PG_EARLY_AB;  // neither operand depends on the row statistics
   CUtensorMap tx, tw;
   if ((st = make_k_map(&tx, x, d, M, d, 128)) != FN_OK) return st;
   if ((st = make_k_map(&tw, Wstar, d, V, d, p.bn / 2)) != FN_OK) return st;
   if ((st = launch_rstd(x, rstd, M, d, eps, s)) != FN_OK) return st;
-  if ((st = launch_pair_gemm<fn::PG_BF16, false, false, fn::CeFwdEpi>(tx, tw, p, ep, sms, dev, s, "cross entropy GEMM")) != FN_OK)
-    return st;
+  const char* what = "cross entropy GEMM";
+  st = p.num_kb > kCeFwdChunk
+           ? launch_pair_gemm<fn::PG_BF16, fn::PgJob<false, false, fn::CeFwdEpi<true>>>(tx, tw, p, ep, sms, dev, s, what)
+           : launch_pair_gemm<fn::PG_BF16, fn::PgJob<false, false, fn::CeFwdEpi<false>>>(tx, tw, p, ep, sms, dev, s, what);
+  if (st != FN_OK) return st;
   cudaError_t e = launch_kernel(fn::k_ce_join, dim3(static_cast<unsigned>((M + 7) / 8)), dim3(256), 0, s, 1,
                                 static_cast<const float2*>(ep.part), static_cast<const float*>(ep.tlogit), ep.targets,
                                 static_cast<float*>(loss), static_cast<float*>(lse), p.M, p.N, 2 * p.num_n_tiles,
@@ -185,6 +206,7 @@ fn_status flashnorm_linear_cross_entropy_backward(const void* g, const void* x, 
   fn::CeRow* rows = reinterpret_cast<fn::CeRow*>(base + c.rows);
   int* rank_of = reinterpret_cast<int*>(base + c.rank_of);
   uint16_t* xc = reinterpret_cast<uint16_t*>(base + c.xc);
+  const fn::CeLive live = {n_live, reinterpret_cast<int*>(base + c.target), reinterpret_cast<float*>(base + c.u)};
   float* cpart = reinterpret_cast<float*>(base + c.part);
   uint16_t* P = reinterpret_cast<uint16_t*>(base + c.P);
   float* acc = reinterpret_cast<float*>(base + c.acc);
@@ -193,7 +215,7 @@ fn_status flashnorm_linear_cross_entropy_backward(const void* g, const void* x, 
   const int64_t per_block = round_up((M + 255) / 256, 8);
   cudaError_t e = launch_kernel(fn::k_ce_pack, dim3(static_cast<unsigned>((M + per_block - 1) / per_block)), dim3(256), 0, s, 1,
                                 static_cast<const uint16_t*>(x), static_cast<const long long*>(targets),
-                                static_cast<const float*>(lse), static_cast<const float*>(g), xc, rows, rank_of, n_live,
+                                static_cast<const float*>(lse), static_cast<const float*>(g), xc, rows, live.target, rank_of, n_live,
                                 static_cast<int>(M), static_cast<int>(d), static_cast<int>(V),
                                 static_cast<int>(per_block), eps, static_cast<long long>(ignore_index));
   if (e != cudaSuccess) return cuda_fail(e, "cross entropy pack launch");
@@ -201,45 +223,39 @@ fn_status flashnorm_linear_cross_entropy_backward(const void* g, const void* x, 
   for (int64_t v0 = 0; v0 < V; v0 += c.piece) {
     const int64_t width = std::min(c.piece, V - v0);
     const uint16_t* W = static_cast<const uint16_t*>(Wstar) + v0 * d;
-    CUtensorMap ta, tb;
+    CUtensorMap ta, tb, ta1, tb1;
     // the logits again, and P from them
-    fn::PairGemmParams p;
-    plan_pair_gemm(&p, M, c.piece, (d + 63) / 64, sms, 32, 1);
+    fn::PairGemmParams p, q;
+    plan_pair_gemm(&p, M, c.piece, (d + 63) / 64, sms, 32);
     p.N = static_cast<int>(width);
     p.num_n_tiles = static_cast<int>((width + p.bn - 1) / p.bn);
-    fn::CeGradParams ge;
-    ge.rows = rows;
-    ge.P = P;
-    ge.cpart = cpart + static_cast<int64_t>(parts) * M;
-    ge.ldp = static_cast<int>(ldp);
-    ge.v0 = static_cast<int>(v0);
-    parts += 2 * p.num_n_tiles;
     p.live = n_live;
+    const fn::CeGradParams ge = {rows, P, cpart + static_cast<int64_t>(parts) * M, static_cast<int>(ldp), static_cast<int>(v0), live.u};
+    parts += 2 * p.num_n_tiles;
     if ((st = make_k_map(&ta, xc, d, Mp, d, 128)) != FN_OK) return st;
     if ((st = make_k_map(&tb, W, d, width, d, p.bn / 2)) != FN_OK) return st;
-    if ((st = launch_pair_gemm<fn::PG_BF16, false, false, fn::CeGradEpi>(ta, tb, p, ge, sms, dev, s, "cross entropy P")) != FN_OK)
+    if ((st = launch_pair_gemm<fn::PG_BF16, fn::PgJob<false, false, fn::CeGradEpi>>(ta, tb, p, ge, sms, dev, s, "cross entropy P")) != FN_OK)
       return st;
-    // dx += P W*
-    plan_pair_gemm(&p, M, d, (width + 63) / 64, sms, kMnStep, 1);
-    p.ksplit = c.ksplit;
+    // dx += P W* and dW* = P^T x
+    plan_pair_gemm_bn(&p, M, d, (width + 63) / 64, ce_mn_width(d), c.ksplit);
     p.live = n_live;
     const fn::CeDxParams xe = {acc, static_cast<int>(d), v0 > 0};
     if ((st = make_k_map(&ta, P, width, Mp, ldp, 128)) != FN_OK) return st;
     if ((st = make_mn_map(&tb, W, d, width, d)) != FN_OK) return st;
-    if ((st = launch_pair_gemm<fn::PG_BF16, false, true, fn::CeDxEpi>(ta, tb, p, xe, sms, dev, s, "cross entropy dx")) != FN_OK)
-      return st;
-    // dW* = P^T x
-    plan_pair_gemm(&p, width, d, (M + 63) / 64, sms, kMnStep, 1);
-    p.live = n_live;
-    p.live_is_k = 1;
-    const fn::CeDwParams we = {static_cast<uint16_t*>(dWstar) + v0 * d, static_cast<int>(d)};
-    if ((st = make_mn_map(&ta, P, width, Mp, ldp)) != FN_OK) return st;
-    if ((st = make_mn_map(&tb, xc, d, Mp, d)) != FN_OK) return st;
-    if ((st = launch_pair_gemm<fn::PG_BF16, true, true, fn::CeDwEpi>(ta, tb, p, we, sms, dev, s, "cross entropy dW")) != FN_OK)
-      return st;
+    plan_pair_gemm_bn(&q, width, d, (M + 63) / 64, ce_mn_width(d), 1);
+    q.live = n_live;
+    q.live_is_k = 1;
+    q.extra = std::max(1, p.num_kb / p.ksplit / q.num_kb);
+    const fn::CeDwParams we = {live, xc, static_cast<uint16_t*>(dWstar) + v0 * d, static_cast<int>(d), static_cast<int>(v0)};
+    if ((st = make_mn_map(&ta1, P, width, Mp, ldp)) != FN_OK) return st;
+    if ((st = make_mn_map(&tb1, xc, d, Mp, d)) != FN_OK) return st;
+    st = launch_pair_gemm2<fn::PgJob<false, true, fn::CeDxEpi>, fn::PgJob<true, true, fn::CeDwEpi>>(
+        ta, tb, p, xe, ta1, tb1, q, we, sms, dev, s, "cross entropy gradients");
+    if (st != FN_OK) return st;
   }
   e = launch_kernel(fn::k_ce_dx, dim3(static_cast<unsigned>(M)), dim3(256), 0, s, 1, static_cast<const float*>(acc),
-                    static_cast<const float*>(cpart), static_cast<const fn::CeRow*>(rows), static_cast<const uint16_t*>(x),
+                    static_cast<const float*>(cpart), static_cast<const fn::CeRow*>(rows), static_cast<const float*>(live.u),
+                    static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(Wstar),
                     static_cast<const int*>(rank_of), static_cast<uint16_t*>(dx), static_cast<int>(M), static_cast<int>(d),
                     c.ksplit, parts);
   return e == cudaSuccess ? FN_OK : cuda_fail(e, "cross entropy dx launch");

@@ -45,7 +45,7 @@ fn_status check_int8_shape(int64_t M, int64_t d, int64_t N, bool glu) {
 template <bool GLU, bool OUT_F32>
 fn_status launch_int8_pair(const CUtensorMap& ta, const CUtensorMap& tb, const fn::PairGemmParams& p,
                            const fn::Int8EpiParams& ep, int sms, int dev, cudaStream_t s) {
-  return launch_pair_gemm<fn::PG_I8, false, false, fn::Int8Epi<GLU, OUT_F32>>(ta, tb, p, ep, sms, dev, s, "int8 GEMM");
+  return launch_pair_gemm<fn::PG_I8, fn::PgJob<false, false, fn::Int8Epi<GLU, OUT_F32>>>(ta, tb, p, ep, sms, dev, s, "int8 GEMM");
 }
 
 template <bool GLU, bool OUT_F32>
@@ -121,7 +121,7 @@ fn_status run_int8(const void* x, const void* Q, const void* scales, void* y, in
   }
   const int step = glu ? 64 : 32;  // whole epilogue blocks
   fn::PairGemmParams p;
-  plan_pair_gemm(&p, M, n_rows, (d + 127) / 128, sms, step, 1);
+  plan_pair_gemm(&p, M, n_rows, (d + 127) / 128, sms, step);
   p.early = fn::PG_EARLY_B;  // Q does not depend on the row pass
   if ((st = make_u8_map(&tx, xq, d, M, 128)) != FN_OK) return st;
   if ((st = make_u8_map(&tw, Q, d, n_rows, p.bn / 2)) != FN_OK) return st;

@@ -9,13 +9,15 @@
 // to the workspace, and a second kernel joins them in a fixed order.
 // Backward: rows without a target have no gradient, so the live rows are packed first and only they go through the three
 // products (a batch half of prompt or padding costs half; what such rows hold cannot reach dW*). Then, in pieces of the
-// vocabulary, the logits are computed again and leave the chip as the factor both gradients
-// share, P[m, n] = r[m] dl[m, n] in bf16, dl[m, n] = g[m] (exp(l - lse) - [n = t]):
-//     dW*[n, :] = sum_m P[m, n] x[m, :]
-//     dx[m, :]  = sum_n P[m, n] W*[n, :] - x[m, :] (r[m]^2 / d) c[m],   c[m] = sum_n dl[m, n] l[m, n]
-// (the second term is the norm's own share: dr/dx = -r^3 x / d). Rounding P to bf16, half a step of 2^-8 per element
-// against tensor-core speed in both products, is the one narrow rounding before the outputs'; their sums, c and the
-// statistics are fp32.
+// vocabulary, the logits are computed again and leave the chip as the factor both gradients share,
+//     P[m, n] = r[m] dl[m, n] in bf16,   dl[m, n] = g[m] (exp(l - lse) - [n = t]),
+// except for the target's own entry u[m] = r dl[m, t], which stays fp32 (P is 0 there):
+//     dW*[n, :] = sum_m P[m, n] x[m, :] + sum_{m: t[m] = n} u[m] x[m, :]
+//     dx[m, :]  = sum_n P[m, n] W*[n, :] + u[m] W*[t, :] - x[m, :] (r[m]^2 / d) c[m],   c[m] = sum_n dl[m, n] l[m, n]
+// (the last term is the norm's own share: dr/dx = -r^3 x / d). The target's entry is most of a row's gradient and would
+// pass its rounding on to a whole row of dx and dW*: 0.0024 against 0.0017 relative, output rounding included. The other
+// entries' roundings, half a step of 2^-8 each, are independent and average out; tensor-core speed in both products
+// depends on them. Sums, c and the statistics are fp32.
 #pragma once
 
 #include "elementwise.cuh"
@@ -68,57 +70,100 @@ struct CeFwdParams {
   float* tlogit;  // [M] logit of the target
 };
 
+// A thread's columns of a tile are up to four chunks of 32, alternating with the quarter's other warp. HELD: the tile takes
+// several accumulations, whose sums so far stay in registers.
+template <bool HELD>
 struct CeFwdEpi {
   using Params = CeFwdParams;
-  float r2;       // r log2(e): the exponentials are powers of two
+  float rstd, r2;  // r2 = r log2(e): the exponentials are powers of two
   long long tgt;
+  float held[HELD ? 4 : 1][32];
   __device__ __forceinline__ CeFwdEpi(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
     const int row = t.row0 + lane;
-    r2 = row < t.M ? __ldcg(e.rstd + row) * kLog2e : 0.f;
+    rstd = row < t.M ? __ldcg(e.rstd + row) : 0.f;
+    r2 = rstd * kLog2e;
     tgt = row < t.M ? __ldg(e.targets + row) : -1;
+    if (HELD) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) held[HELD ? i : 0][j] = 0.f;
+    }
   }
   __device__ __forceinline__ void run(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
     const int row = t.row0 + lane;
+    const int c00 = 32 * ((t.half + t.turn) & 1);
     float m = -INFINITY, s = 0.f;
-    for (int ch = (t.half + t.turn) & 1; ch * 32 < t.width; ch += 2) {
-      const int c0 = ch * 32;
-      uint32_t v[2][16];
+    auto load = [&](int c0, uint32_t (&v)[2][16]) {
       tmem_ld16(t.t_row + c0, v[0]);
       tmem_ld16(t.t_row + c0 + 16, v[1]);
       tmem_ld_wait();
       reg_fence16(v[0]);
       reg_fence16(v[1]);
-      float l[32];
+    };
+    if (HELD && t.chunk < t.chunks - 1) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) l[j] = __uint_as_float(v[j >> 4][j & 15]) * r2;
-      if (c0 + 32 > t.width) {  // columns past the vocabulary take no part
+      for (int i = 0; i < 4; ++i) {
+        uint32_t v[2][16];
+        if (c00 + 64 * i >= t.width) continue;
+        load(c00 + 64 * i, v);
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (c0 + j >= t.width) l[j] = -INFINITY;
+        for (int j = 0; j < 32; ++j) held[HELD ? i : 0][j] += __uint_as_float(v[j >> 4][j & 15]);
+      }
+      return;
+    }
+#pragma unroll(HELD ? 4 : 1)
+    for (int i = 0; i < 4; ++i) {
+      const int c0 = c00 + 64 * i;
+      if (c0 >= t.width) break;
+      float z[32];
+      {
+        uint32_t v[2][16];
+        load(c0, v);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) z[j] = (HELD ? held[HELD ? i : 0][j] : 0.f) + __uint_as_float(v[j >> 4][j & 15]);
       }
       const long long at = tgt - (t.n0 + c0);
       if (at >= 0 && at < 32) {
         float lt = 0.f;
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-          if (at == j) lt = __uint_as_float(v[j >> 4][j & 15]);
-        if (c0 + at < t.width) e.tlogit[row] = lt * __ldcg(e.rstd + row);
+          if (at == j) lt = z[j];
+        if (c0 + at < t.width) e.tlogit[row] = lt * rstd;
       }
-      float mc = l[0];
+      const bool edge = c0 + 32 > t.width;  // columns past the vocabulary take no part
+      if (edge) {
 #pragma unroll
-      for (int j = 1; j < 32; ++j) mc = fmaxf(mc, l[j]);
-      const float mn = fmaxf(m, mc);
+        for (int j = 1; j < 32; ++j)
+          if (c0 + j >= t.width) z[j] = z[0];
+      }
+      float mc = z[0];
+#pragma unroll
+      for (int j = 1; j < 32; ++j) mc = fmaxf(mc, z[j]);
+      const float mn = fmaxf(m, mc * r2);
       const float base = mn == -INFINITY ? 0.f : mn;  // a row of -inf so far: 2^(-inf) = 0, not NaN
-      float a0 = 0.f, a1 = 0.f;
+      const uint64_t rr = pack_f32x2(r2, r2), nb = pack_f32x2(-base, -base);
+      uint64_t a0 = 0, a1 = 0;
 #pragma unroll
-      for (int j = 0; j < 32; j += 2) {
-        a0 += ex2(l[j] - base);
-        a1 += ex2(l[j + 1] - base);
+      for (int j = 0; j < 32; j += 4) {
+        const float2 q0 = unpack_f32x2(fma_f32x2(pack_f32x2(z[j], z[j + 1]), rr, nb));
+        const float2 q1 = unpack_f32x2(fma_f32x2(pack_f32x2(z[j + 2], z[j + 3]), rr, nb));
+        float e0 = ex2(q0.x), e1 = ex2(q0.y), e2 = ex2(q1.x), e3 = ex2(q1.y);
+        if (edge) {
+          if (c0 + j >= t.width) e0 = 0.f;
+          if (c0 + j + 1 >= t.width) e1 = 0.f;
+          if (c0 + j + 2 >= t.width) e2 = 0.f;
+          if (c0 + j + 3 >= t.width) e3 = 0.f;
+        }
+        a0 = add_f32x2(a0, pack_f32x2(e0, e1));
+        a1 = add_f32x2(a1, pack_f32x2(e2, e3));
       }
-      s = s * ex2(m - base) + (a0 + a1);
+      const float2 sum = unpack_f32x2(add_f32x2(a0, a1));
+      s = s * ex2(m - base) + (sum.x + sum.y);
       m = mn;
     }
-    if (row < t.M) e.part[static_cast<size_t>(row) * (2 * p.num_n_tiles) + 2 * t.nt + t.half] = make_float2(m, s);
+    if (row < t.M)
+      e.part[static_cast<size_t>(row) * (2 * p.num_n_tiles) + 2 * t.nt + t.half] = make_float2(m, s);
   }
 };
 
@@ -169,6 +214,13 @@ struct __align__(16) CeRow {
   int target;
 };
 
+// What the other two products and the last kernel need of them.
+struct CeLive {
+  const int* n_live;
+  int* target;  // [live rows]
+  float* u;     // r dl of the target's entry
+};
+
 constexpr int kCeIgnored = -1, kCeBad = -2;  // in place of a row's rank among the live ones
 
 // Packs the live rows in order: xc[rank] = x[m], rows[rank], rank_of[m], and their number. Rows up to the next multiple of
@@ -177,7 +229,8 @@ constexpr int kCeIgnored = -1, kCeBad = -2;  // in place of a row's rank among t
 __global__ void __launch_bounds__(256) k_ce_pack(const uint16_t* __restrict__ x, const long long* __restrict__ targets,
                                                  const float* __restrict__ lse, const float* __restrict__ g,
                                                  uint16_t* __restrict__ xc, CeRow* __restrict__ rows,
-                                                 int* __restrict__ rank_of, int* __restrict__ n_live, int M, int K, int V,
+                                                 int* __restrict__ target, int* __restrict__ rank_of,
+                                                 int* __restrict__ n_live, int M, int K, int V,
                                                  int rows_per_block, float eps, long long ignore) {
   grid_dep_wait();
   grid_dep_launch();
@@ -188,7 +241,20 @@ __global__ void __launch_bounds__(256) k_ce_pack(const uint16_t* __restrict__ x,
     return t != ignore && target_is_class(t, V);
   };
   const int b0 = static_cast<int>(blockIdx.x) * rows_per_block;
+  const int per_warp = rows_per_block >> 3, m0 = b0 + warp * per_warp;
+  const int chunks = K >> 3;
+  // a row's first kHeld * 256 elements go through registers; those of the warp's first row are loaded ahead of the count
+  constexpr int kHeld = 16;
+  uint4 held[kHeld];
+  auto load_row = [&](int m) {
+    const uint4* src = reinterpret_cast<const uint4*>(x + static_cast<size_t>(m) * K);
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      held[i] = lane + 32 * i < chunks ? __ldg(src + lane + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  if (m0 < M) load_row(m0);
   int n = 0;
+#pragma unroll 8
   for (int m = threadIdx.x; m < b0; m += 256) n += live_at(m);
   n = __reduce_add_sync(0xffffffffu, n);
   if (lane == 0) counts[warp] = n;
@@ -196,14 +262,12 @@ __global__ void __launch_bounds__(256) k_ce_pack(const uint16_t* __restrict__ x,
   int base = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) base += counts[i];
-  const int per_warp = rows_per_block >> 3, m0 = b0 + warp * per_warp;
   auto count = [&](int from, int to) {
     int c = 0;
     for (int m = from + lane; m < to; m += 32) c += live_at(m);
     return __reduce_add_sync(0xffffffffu, c);
   };
   int rank = base + count(b0, min(m0, M));
-  const int chunks = K >> 3;
   for (int m = m0; m < min(m0 + per_warp, M); ++m) {
     const long long t = __ldg(targets + m);
     const bool live = t != ignore && target_is_class(t, V);
@@ -212,10 +276,7 @@ __global__ void __launch_bounds__(256) k_ce_pack(const uint16_t* __restrict__ x,
     const uint4* src = reinterpret_cast<const uint4*>(x + static_cast<size_t>(m) * K);
     uint4* dst = reinterpret_cast<uint4*>(xc + static_cast<size_t>(rank) * K);
     float s0 = 0.f, s1 = 0.f;
-#pragma unroll 4
-    for (int c = lane; c < chunks; c += 32) {
-      const uint4 v = __ldg(src + c);
-      dst[c] = v;
+    auto take = [&](const uint4& v) {
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -223,6 +284,18 @@ __global__ void __launch_bounds__(256) k_ce_pack(const uint16_t* __restrict__ x,
         s0 = fmaf(a, a, s0);
         s1 = fmaf(b, b, s1);
       }
+    };
+    if (m != m0) load_row(m);
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      if (lane + 32 * i < chunks) dst[lane + 32 * i] = held[i];
+      take(held[i]);
+    }
+#pragma unroll 4
+    for (int c = lane + 32 * kHeld; c < chunks; c += 32) {
+      const uint4 v = __ldg(src + c);
+      dst[c] = v;
+      take(v);
     }
     const float ss = warp_sum(s0 + s1);
     if (lane == 0) {
@@ -232,6 +305,7 @@ __global__ void __launch_bounds__(256) k_ce_pack(const uint16_t* __restrict__ x,
       r.g = __ldg(g + m);
       r.target = static_cast<int>(t);
       rows[rank] = r;
+      target[rank] = r.target;
     }
     ++rank;
   }
@@ -252,6 +326,7 @@ struct CeGradParams {
   float* cpart;    // [2 column tiles][M] partial c, this piece's
   int ldp;         // a multiple of 64: rows of P start on whole 128-byte lines
   int v0;          // first column of the piece within the vocabulary
+  float* u;        // CeLive's
 };
 
 struct CeGradEpi {
@@ -259,7 +334,8 @@ struct CeGradEpi {
   CeRow q;
   __device__ __forceinline__ CeGradEpi(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
     const int row = t.row0 + lane;
-    q.rstd = q.nlse2 = q.g = 0.f;
+    q.rstd = q.g = 0.f;
+    q.nlse2 = -INFINITY;  // past the live rows every exponential is 0
     q.target = -1;
     if (row < t.M) {
       const float4 v = __ldcg(reinterpret_cast<const float4*>(e.rows + row));
@@ -268,8 +344,11 @@ struct CeGradEpi {
   }
   __device__ __forceinline__ void run(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
     const int row = t.row0 + lane;
-    const float r2 = q.rstd * kLog2e;
-    float c = 0.f;
+    const float r2 = q.rstd * kLog2e, gr = q.g * q.rstd;
+    const uint64_t rr = pack_f32x2(r2, r2), nl = pack_f32x2(q.nlse2, q.nlse2), gg = pack_f32x2(gr, gr);
+    uint64_t c2 = 0;  // sum of exp(l - lse) z; c = g r times it
+    float ct = 0.f;   // the target's -z
+    const int t0 = q.target - (e.v0 + t.n0);  // the target's column in this tile, if it has it
     for (int ch = (t.half + t.turn) & 1; ch * 32 < t.width; ch += 2) {
       const int c0 = ch * 32;
       uint32_t v[2][16];
@@ -278,48 +357,186 @@ struct CeGradEpi {
       tmem_ld_wait();
       reg_fence16(v[0]);
       reg_fence16(v[1]);
-      const int at = q.target - (e.v0 + t.n0 + c0);
-      float o[32];
+      const bool edge = t.row0 + 32 > t.M || c0 + 32 > t.width;
+      if (edge) {  // whatever lies past the live rows or the vocabulary takes no part
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const float z = __uint_as_float(v[j >> 4][j & 15]);
-        float dl = ex2(fmaf(z, r2, q.nlse2));
-        if (at == j) dl -= 1.0f;
-        dl *= q.g;
-        if (c0 + j >= t.width || row >= t.M) dl = 0.f;
-        c = fmaf(dl, z, c);
-        o[j] = dl * q.rstd;
+        for (int j = 0; j < 32; ++j)
+          if (row >= t.M || c0 + j >= t.width) v[j >> 4][j & 15] = 0u;
+      }
+      uint32_t w[16];
+      float2 o[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const uint64_t z = pack_f32x2(__uint_as_float(v[j >> 3][2 * (j & 7)]), __uint_as_float(v[j >> 3][2 * (j & 7) + 1]));
+        const float2 a = unpack_f32x2(fma_f32x2(z, rr, nl));
+        const uint64_t ex = pack_f32x2(ex2(a.x), ex2(a.y));
+        c2 = fma_f32x2(ex, z, c2);
+        o[j] = unpack_f32x2(mul_f32x2(ex, gg));
+      }
+      if (edge) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (c0 + j >= t.width) {
+            if (j & 1) o[j >> 1].y = 0.f; else o[j >> 1].x = 0.f;
+          }
+      }
+      const int at = t0 - c0;
+      if (row < t.M && at >= 0 && at < 32 && c0 + at < t.width) {  // the target's entry: kept in fp32, 0 in P
+        float z = 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (at == j) {
+            z = __uint_as_float(v[j >> 4][j & 15]);
+            if (j & 1) o[j >> 1].y = 0.f; else o[j >> 1].x = 0.f;
+          }
+        e.u[row] = gr * (ex2(fmaf(z, r2, q.nlse2)) - 1.0f);
+        ct = -z;
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        pg_put(t.stage, lane, j, make_uint4(pack_bf16x2(o[8 * j], o[8 * j + 1]), pack_bf16x2(o[8 * j + 2], o[8 * j + 3]),
-                                            pack_bf16x2(o[8 * j + 4], o[8 * j + 5]), pack_bf16x2(o[8 * j + 6], o[8 * j + 7])));
+      for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(o[j].x, o[j].y);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) pg_put(t.stage, lane, j, make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
       // zeros up to the end of the stage of 64 rows that dW*'s product reads
       pg_flush(t.stage, lane, e.P, static_cast<size_t>(e.ldp) * 2, t.row0, (t.M + 63) & ~63, 2ll * (t.n0 + c0), 2ll * e.ldp);
     }
-    if (row < t.M) e.cpart[static_cast<size_t>(2 * t.nt + t.half) * p.M + row] = c * q.rstd;
+    const float2 cs = unpack_f32x2(c2);
+    if (row < t.M) e.cpart[static_cast<size_t>(2 * t.nt + t.half) * p.M + row] = gr * ((cs.x + cs.y) + ct);
   }
 };
 
-// dW*: the product as it is, rounded to bf16 once.
+// dW*: the product plus the target entries' share, rounded to bf16 once. Of a warp's 32 vocabulary rows few are a target:
+// while the MMAs run it looks through the live rows' targets (two loads of 32 per stage of K, sixteen in flight) and lists
+// those it finds, lane k the k-th. The rows found are added in their order, eight at a time: the lanes load the chunk's 32
+// columns of u x (for the first eight one chunk ahead) and pass them through the staging buffer to the lane whose row it
+// is. A warp with more than 32 hits (a frequent token) looks for the further ones again in every chunk.
 struct CeDwParams {
+  CeLive live;
+  const uint16_t* xc;  // [live rows][ldy]
   uint16_t* y;
   int ldy;
+  int v0;
+};
+struct CeDwHits {
+  int n;     // how many, the same in every lane
+  int next;  // first live row not looked at
+  int r;     // lane k: live row of hit k, its vocabulary row within the warp's, its u
+  int row;
+  float u;
 };
 struct CeDwEpi {
   using Params = CeDwParams;
-  __device__ __forceinline__ CeDwEpi(const Params&, const PairGemmParams&, const PgTile&, int) {}
+  int base, live;  // first vocabulary row of the warp; live rows
+  CeDwHits first;
+  float val[8];  // of the first eight hits, for the chunk to come
+
+  __device__ __forceinline__ CeDwHits look(const Params& e, int from, int lane) const {
+    CeDwHits h = {0, live, 0, 0, 0.f};
+    for (int r0 = from & ~31; r0 < live; r0 += 512) {
+      int t[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int r = r0 + 32 * i + lane;
+        t[i] = r >= from && r < live ? __ldcg(e.live.target + r) - base : -1;
+      }
+      bool any = false;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) any |= static_cast<unsigned>(t[i]) < 32u;
+      if (!__any_sync(0xffffffffu, any)) continue;
+#pragma unroll 1
+      for (int i = 0; i < 16; ++i) {
+        int ti = t[0];
+#pragma unroll
+        for (int k = 0; k < 15; ++k) t[k] = t[k + 1];
+        unsigned hits = __ballot_sync(0xffffffffu, static_cast<unsigned>(ti) < 32u);
+        for (; hits != 0; hits &= hits - 1) {
+          const int src = __ffs(hits) - 1, row = __shfl_sync(0xffffffffu, ti, src);
+          if (h.n == 32) {
+            h.next = r0 + 32 * i + src;
+            goto done;
+          }
+          if (lane == h.n) h.r = r0 + 32 * i + src, h.row = row;
+          ++h.n;
+        }
+      }
+    }
+  done:
+    if (lane < h.n) h.u = __ldcg(e.live.u + h.r);
+    return h;
+  }
+  // u x of hits k0 .. k0+7 at the lane's column
+  __device__ __forceinline__ void fetch(const Params& e, const CeDwHits& h, int k0, int col, int N) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int r = __shfl_sync(0xffffffffu, h.r, (k0 + k) & 31);
+      const float u = __shfl_sync(0xffffffffu, h.u, (k0 + k) & 31);
+      val[k] = k0 + k < h.n && col < N ? u * bf16lo_to_f32(__ldg(e.xc + static_cast<size_t>(r) * e.ldy + col)) : 0.f;
+    }
+  }
+  // Slot k of the staging buffer holds hit k0 + k: 32 floats, piece j at (j + k) % 8.
+  __device__ __forceinline__ void stage(const PgTile& t, int lane) const {
+    float* slots = reinterpret_cast<float*>(t.stage);
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) slots[k * 32 + (((lane >> 2) + k) & 7) * 4 + (lane & 3)] = val[k];
+    __syncwarp();
+  }
+  __device__ __forceinline__ void add(const CeDwHits& h, int k0, const PgTile& t, int lane, uint32_t (&v)[2][16]) const {
+    const float* slots = reinterpret_cast<const float*>(t.stage);
+    for (int k = 0; k0 + k < h.n && k < 8; ++k) {
+      if (__shfl_sync(0xffffffffu, h.row, k0 + k) != lane) continue;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float4 a = *reinterpret_cast<const float4*>(slots + k * 32 + ((j + k) & 7) * 4);
+        uint32_t* w = &v[j >> 2][4 * (j & 3)];
+        w[0] = __float_as_uint(__uint_as_float(w[0]) + a.x);
+        w[1] = __float_as_uint(__uint_as_float(w[1]) + a.y);
+        w[2] = __float_as_uint(__uint_as_float(w[2]) + a.z);
+        w[3] = __float_as_uint(__uint_as_float(w[3]) + a.w);
+      }
+    }
+    __syncwarp();
+  }
+
+  __device__ __forceinline__ CeDwEpi(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
+    base = e.v0 + t.row0;
+    live = __ldcg(e.live.n_live);
+    first = look(e, 0, lane);
+    if (first.n > 0) fetch(e, first, 0, t.n0 + 32 * ((t.half + t.turn) & 1) + lane, p.N);
+  }
   __device__ __forceinline__ void run(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
     for (int ch = (t.half + t.turn) & 1; ch * 32 < t.width; ch += 2) {
       uint32_t v[2][16];
       tmem_ld16(t.t_row + ch * 32, v[0]);
       tmem_ld16(t.t_row + ch * 32 + 16, v[1]);
+      const int col = t.n0 + ch * 32 + lane;
+      if (first.n > 0) {
+        stage(t, lane);
+        if (first.n <= 8) fetch(e, first, 0, col + 64, p.N);
+      }
       tmem_ld_wait();
       reg_fence16(v[0]);
       reg_fence16(v[1]);
       if (t.empty) {  // no live rows
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j >> 4][j & 15] = 0u;
+      }
+      if (first.n > 0) {
+        add(first, 0, t, lane, v);
+        for (int k0 = 8; k0 < first.n; k0 += 8) {
+          fetch(e, first, k0, col, p.N);
+          stage(t, lane);
+          add(first, k0, t, lane, v);
+        }
+        for (int from = first.next; from < live;) {
+          const CeDwHits h = look(e, from, lane);
+          for (int k0 = 0; k0 < h.n; k0 += 8) {
+            fetch(e, h, k0, col, p.N);
+            stage(t, lane);
+            add(h, k0, t, lane, v);
+          }
+          from = h.next;
+        }
+        if (first.n > 8) fetch(e, first, 0, col + 64, p.N);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -373,10 +590,11 @@ struct CeDxEpi {
   }
 };
 
-// dx[m, :] = sum of the planes - x[m, :] (r^2 / d) c[m], one block per row; planes and partial sums c by the row's rank among
+// dx[m, :] = sum of the planes + u[m] W*[t, :] - x[m, :] (r^2 / d) c[m], one block per row; planes and partial sums c by the row's rank among
 // the live ones, in a fixed order.
 __global__ void __launch_bounds__(256) k_ce_dx(const float* __restrict__ acc, const float* __restrict__ cpart,
-                                               const CeRow* __restrict__ rows, const uint16_t* __restrict__ x,
+                                               const CeRow* __restrict__ rows, const float* __restrict__ u,
+                                               const uint16_t* __restrict__ x, const uint16_t* __restrict__ W,
                                                const int* __restrict__ rank_of, uint16_t* __restrict__ dx, int M, int K,
                                                int planes, int parts) {
   __shared__ float red[8];
@@ -398,7 +616,8 @@ __global__ void __launch_bounds__(256) k_ce_dx(const float* __restrict__ acc, co
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = c;
   __syncthreads();
   c = ((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7]));
-  const float r = __ldcg(&rows[rank].rstd);
+  const float r = __ldcg(&rows[rank].rstd), ut = __ldcg(u + rank);
+  const uint4* wr = reinterpret_cast<const uint4*>(W + static_cast<size_t>(__ldcg(&rows[rank].target)) * K);
   const float k = r * r / static_cast<float>(K) * c;
   const uint4* xr = reinterpret_cast<const uint4*>(x + static_cast<size_t>(row) * K);
   for (int i = threadIdx.x; i < (K >> 3); i += 256) {
@@ -409,7 +628,11 @@ __global__ void __launch_bounds__(256) k_ce_dx(const float* __restrict__ acc, co
       a = make_float4(a.x + p.x, a.y + p.y, a.z + p.z, a.w + p.w);
       b = make_float4(b.x + q.x, b.y + q.y, b.z + q.z, b.w + q.w);
     }
-    const uint4 v = xr[i];
+    const uint4 v = xr[i], w = __ldg(wr + i);
+    a = make_float4(fmaf(ut, bf16lo_to_f32(w.x), a.x), fmaf(ut, bf16hi_to_f32(w.x), a.y), fmaf(ut, bf16lo_to_f32(w.y), a.z),
+                    fmaf(ut, bf16hi_to_f32(w.y), a.w));
+    b = make_float4(fmaf(ut, bf16lo_to_f32(w.z), b.x), fmaf(ut, bf16hi_to_f32(w.z), b.y), fmaf(ut, bf16lo_to_f32(w.w), b.z),
+                    fmaf(ut, bf16hi_to_f32(w.w), b.w));
     dst[i] = make_uint4(pack_bf16x2(fmaf(-k, bf16lo_to_f32(v.x), a.x), fmaf(-k, bf16hi_to_f32(v.x), a.y)),
                         pack_bf16x2(fmaf(-k, bf16lo_to_f32(v.y), a.z), fmaf(-k, bf16hi_to_f32(v.y), a.w)),
                         pack_bf16x2(fmaf(-k, bf16lo_to_f32(v.z), b.x), fmaf(-k, bf16hi_to_f32(v.z), b.y)),

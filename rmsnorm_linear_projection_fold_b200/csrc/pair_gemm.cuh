@@ -11,10 +11,22 @@
 //
 // Operands. bf16 (kind::f16, fp32 accumulator) or int8 (kind::i8, exact int32 accumulator); a stage holds 128
 // bytes of K per row (64 bf16, 128 int8). A bf16 operand may also be "MN-major": stored [K][rows], as a
-// transposed factor of a gradient is; its stage is boxes of 64 k x 64 rows, each 64 lines of 128 bytes.
+// transposed factor of a gradient is; its stage is boxes of 64 k x 64 rows, each 64 lines of 128 bytes. Tiles of an
+// MN-major B are multiples of 128 wide, so that every box starts on a 128-byte line: boxes that start in the middle of one
+// took 1.8 times as long (517 x 576 outputs, k = 50257: 125 against 69 us with narrower, aligned tiles). The last column
+// tile is only as wide as its columns need.
+//
+// Two products that share nothing but the grid may run as one launch (jobs 0 and 1): a pair takes its items of job 0,
+// usually few and long, and then its share of job 1's many short ones, which evens out what job 0 left uneven.
+//
+// Accumulation. The tensor core adds into its fp32 accumulator without rounding to nearest, so a long sum drifts (at
+// k = 4096 a logit's relative error is near 4e-6). An epilogue that needs better takes the sum in chunks of `kchunk` stages,
+// which it adds in its own registers.
 //
 // Warps: 0 = TMA producer, 1 = MMA issuer (leader) and tensor memory, 2..9 = epilogue, two per lane quarter.
 #pragma once
+
+#include <type_traits>
 
 #include "sm100.cuh"
 
@@ -32,7 +44,8 @@ __host__ __device__ constexpr int pair_gemm_smem_bytes() {
 struct PairGemmParams {
   int M, N;         // rows and columns of C
   int num_kb;       // stages along K
-  int bn;           // tile width: a multiple of 32, at most 256
+  int kchunk;       // stages per accumulation (an epilogue that takes only whole sums: num_kb)
+  int bn;           // tile width: a multiple of 32 (MN-major B: of 128), at most 256
   int num_m_tiles;  // of 256 rows
   int num_n_tiles;
   int band;         // row tiles per band
@@ -40,6 +53,7 @@ struct PairGemmParams {
   int early;        // PgEarly: operands that do not depend on the previous kernel of the stream
   int live_is_k;    // what *live counts: rows of C, or (1) k
   const int* live;  // null, or a count on the device that replaces M (at most M) or num_kb (at most so many stages)
+  int extra;        // job 1: items that a pair with one item less of job 0 takes first, in exchange
 };
 
 // Operands that may be fetched before the previous kernel has completed. That kernel must itself have waited for all
@@ -86,6 +100,7 @@ struct PgTile {
   int nt, kz;      // column tile and K range
   int M;           // rows of C
   bool empty;      // no k at all: the accumulator holds nothing and counts as zero
+  int chunk, chunks;  // accumulations of this tile: which one run() has before it, and how many
   uint8_t* stage;  // this warp's staging buffer
 };
 
@@ -110,11 +125,50 @@ __device__ __forceinline__ void pg_flush(uint8_t* stage, int lane, void* y, size
   __syncwarp();  // the staging buffer is read before the next block overwrites it
 }
 
-template <int KIND, bool A_MN, bool B_MN, class Epi>
-__global__ void __launch_bounds__(kPgThreads, 1)
-    k_pair_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, PairGemmParams p,
-                typename Epi::Params ep) {
-  static_assert(KIND == PG_BF16 || (!A_MN && !B_MN), "8-bit operands are K-major");
+// One product: operand layouts and epilogue.
+template <bool A_MN_, bool B_MN_, class Epi_>
+struct PgJob {
+  static constexpr bool A_MN = A_MN_, B_MN = B_MN_;
+  using Epi = Epi_;
+  using Params = typename Epi_::Params;
+};
+
+// The empty second job.
+struct PgNoEpi {
+  struct Params {};
+  __device__ __forceinline__ PgNoEpi(const Params&, const PairGemmParams&, const PgTile&, int) {}
+  __device__ __forceinline__ void run(const Params&, const PairGemmParams&, const PgTile&, int) {}
+};
+using PgNoJob = PgJob<false, false, PgNoEpi>;
+
+// What the device knows of one job: sizes after *live has been read, and where item t lies.
+struct PgPlan {
+  int rows, num_kb, m_tiles, tiles, items;
+  __device__ __forceinline__ PgPlan(const PairGemmParams& p, int k_per_stage) {
+    rows = p.M, num_kb = p.num_kb;
+    if (p.live != nullptr) {
+      const int live = __ldcg(p.live);
+      if (p.live_is_k)
+        num_kb = (live + k_per_stage - 1) / k_per_stage;
+      else
+        rows = live;
+    }
+    m_tiles = (rows + 255) >> 8;
+    tiles = m_tiles * p.num_n_tiles;
+    items = tiles * p.ksplit;
+  }
+};
+
+struct PgItem {
+  int job, mt, nt, kz, kb0, kb1, width, wide;  // width: columns; wide: the MMA's N
+};
+
+template <int KIND, class J0, class J1, bool TWO>
+__device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tm_a0, const CUtensorMap& tm_b0, const PairGemmParams& p0,
+                                               const typename J0::Params& ep0, const CUtensorMap& tm_a1,
+                                               const CUtensorMap& tm_b1, const PairGemmParams& p1,
+                                               const typename J1::Params& ep1) {
+  static_assert(KIND == PG_BF16 || (!J0::A_MN && !J0::B_MN && !TWO), "8-bit operands are K-major");
   constexpr int kElem = KIND == PG_I8 ? 1 : 2;
   constexpr int kK = 128 / kElem;  // k per stage
 
@@ -151,8 +205,12 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     mbar_init_fence();
   }
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tm_a);
-    tma_prefetch_desc(&tm_b);
+    tma_prefetch_desc(&tm_a0);
+    tma_prefetch_desc(&tm_b0);
+    if (TWO) {
+      tma_prefetch_desc(&tm_a1);
+      tma_prefetch_desc(&tm_b1);
+    }
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 512);
@@ -164,35 +222,52 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
   // The previous kernel's outputs (our inputs, or buffers we overwrite) are complete. Early operands do not wait for that;
-  // their producer does once it needs the others, the epilogue always does.
-  if (p.early == PG_EARLY_NONE || warp >= 2) grid_dep_wait();
+  // their producer does once it needs the others, the epilogue always does. Early operands exclude *live and a second job.
+  if (p0.early == PG_EARLY_NONE || warp >= 2) grid_dep_wait();
 
-  int rows = p.M, num_kb = p.num_kb;
-  if (p.live != nullptr) {  // never with early operands
-    const int live = __ldcg(p.live);
-    if (p.live_is_k)
-      num_kb = (live + kK - 1) / kK;
-    else
-      rows = live;
-  }
-  const int num_m_tiles = (rows + 255) >> 8;
   const int cl = static_cast<int>(blockIdx.x) >> 1, ncl = static_cast<int>(gridDim.x) >> 1;
-  const int tiles = num_m_tiles * p.num_n_tiles;
-  const int items = tiles * p.ksplit;
-  // Item t: its row and column tile (bands of p.band row tiles, row tile fastest) and K range.
-  auto item_at = [&](int t, int& mt, int& nt, int& kz, int& kb0, int& kb1) {
-    kz = t / tiles;
-    const int u = t - kz * tiles;
+  const PgPlan plan0(p0, kK);
+  const PgPlan plan1 = TWO ? PgPlan(p1, kK) : plan0;
+  // Items t of a job: bands of `band` row tiles, row tile fastest, K ranges outermost.
+  auto place = [&](const PairGemmParams& p, const PgPlan& pl, bool b_mn, int t, PgItem& it) {
+    it.kz = t / pl.tiles;
+    const int u = t - it.kz * pl.tiles;
     const int per_band = p.band * p.num_n_tiles;
     const int b = u / per_band, r = u - b * per_band;
-    const int in_band = min(p.band, num_m_tiles - b * p.band);
-    mt = b * p.band + r % in_band;
-    nt = r / in_band;
-    kb0 = static_cast<int>(static_cast<long long>(kz) * num_kb / p.ksplit);
-    kb1 = static_cast<int>(static_cast<long long>(kz + 1) * num_kb / p.ksplit);
+    const int in_band = min(p.band, pl.m_tiles - b * p.band);
+    it.mt = b * p.band + r % in_band;
+    it.nt = r / in_band;
+    it.kb0 = static_cast<int>(static_cast<long long>(it.kz) * pl.num_kb / p.ksplit);
+    it.kb1 = static_cast<int>(static_cast<long long>(it.kz + 1) * pl.num_kb / p.ksplit);
+    it.width = min(p.bn, p.N - it.nt * p.bn);
+    it.wide = b_mn ? (it.width + 127) & ~127 : (it.width + 31) & ~31;
   };
-  const int bh = p.bn / 2;                // B rows per CTA
-  const int b_boxes = (bh + 63) / 64;     // MN-major: 64-wide boxes per CTA
+  // Item i of this pair. Job 0 goes round robin. Of job 1, the pairs that got one item less of job 0 first take `extra`
+  // items each, the rest goes round robin.
+  const int n0 = (plan0.items - cl + ncl - 1) / ncl;  // 0 or less: none
+  const int heavy = plan0.items % ncl;
+  const int lights = heavy ? ncl - heavy : 0;
+  const int light_extra = TWO && lights ? min(p1.extra, plan1.items / lights) : 0;
+  auto item_at = [&](int i, PgItem& it) {
+    if (!TWO || i < n0) {
+      const int t = cl + i * ncl;
+      if (t >= plan0.items) return false;
+      it.job = 0;
+      place(p0, plan0, J0::B_MN, t, it);
+      return true;
+    }
+    int j = i - max(n0, 0);
+    int t;
+    if (heavy && cl >= heavy) {
+      t = j < light_extra ? (cl - heavy) + j * lights : lights * light_extra + cl + (j - light_extra) * ncl;
+    } else {
+      t = lights * light_extra + cl + j * ncl;
+    }
+    if (t >= plan1.items) return false;
+    it.job = 1;
+    place(p1, plan1, J1::B_MN, t, it);
+    return true;
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer (both CTAs)
@@ -200,52 +275,59 @@ __global__ void __launch_bounds__(kPgThreads, 1)
       int s = 0, issued = 0;
       uint32_t ph = 0;
       bool ok = true;
-      const uint32_t stage_bytes =
-          static_cast<uint32_t>(kPgTileBytes + (B_MN ? b_boxes * 8192 : bh * 128));
-      auto load_a = [&](int st, int kb, int m0) {
+      auto bytes_of = [&](const PgItem& it, const PairGemmParams& p, bool b_mn) {
+        return static_cast<uint32_t>(kPgTileBytes + (b_mn ? it.wide * 64 : p.bn * 64));
+      };
+      auto load_a = [&](bool mn, const CUtensorMap& tm, int st, int kb, int m0) {
         const uint32_t bar = dsmem_addr(&full[st], 0);
-        if (A_MN) {
-          tma_load_2d_pair(sA + st * kPgTileBytes, &tm_a, bar, m0, kb * kK);
-          tma_load_2d_pair(sA + st * kPgTileBytes + 8192, &tm_a, bar, m0 + 64, kb * kK);
+        if (mn) {
+          tma_load_2d_pair(sA + st * kPgTileBytes, &tm, bar, m0, kb * kK);
+          tma_load_2d_pair(sA + st * kPgTileBytes + 8192, &tm, bar, m0 + 64, kb * kK);
         } else {
-          tma_load_2d_pair(sA + st * kPgTileBytes, &tm_a, bar, kb * kK, m0);
+          tma_load_2d_pair(sA + st * kPgTileBytes, &tm, bar, kb * kK, m0);
         }
       };
-      auto load_b = [&](int st, int kb, int n0) {
+      // K-major: one box of bn / 2 rows, of which a narrower last tile uses the first ones
+      auto load_b = [&](bool mn, const CUtensorMap& tm, int st, int kb, int n0, int wide) {
         const uint32_t bar = dsmem_addr(&full[st], 0);
-        if (B_MN) {
-          for (int j = 0; j < b_boxes; ++j)
-            tma_load_2d_pair(sB + st * kPgTileBytes + j * 8192, &tm_b, bar, n0 + 64 * j, kb * kK);
+        if (mn) {
+          for (int j = 0; j < wide / 128; ++j)
+            tma_load_2d_pair(sB + st * kPgTileBytes + j * 8192, &tm, bar, n0 + 64 * j, kb * kK);
         } else {
-          tma_load_2d_pair(sB + st * kPgTileBytes, &tm_b, bar, kb * kK, n0);
+          tma_load_2d_pair(sB + st * kPgTileBytes, &tm, bar, kb * kK, n0);
         }
       };
+      PgItem it;
       int ahead = 0;  // stages whose B is already on its way
-      if (p.early == PG_EARLY_B && cl < items) {
-        int mt, nt, kz, kb0, kb1;
-        item_at(cl, mt, nt, kz, kb0, kb1);
-        ahead = min(kPgStages, kb1 - kb0);
-        for (int st = 0; st < ahead; ++st) {  // every stage is free at the start
-          if (leader) mbar_arrive_expect_tx(&full[st], 2 * stage_bytes);
-          load_b(st, kb0 + st, nt * p.bn + static_cast<int>(rank) * bh);
+      if (!TWO && p0.early == PG_EARLY_B) {
+        if (item_at(0, it)) {
+          ahead = min(kPgStages, it.kb1 - it.kb0);
+          for (int st = 0; st < ahead; ++st) {  // every stage is free at the start
+            if (leader) mbar_arrive_expect_tx(&full[st], 2 * bytes_of(it, p0, J0::B_MN));
+            load_b(J0::B_MN, tm_b0, st, it.kb0 + st, it.nt * p0.bn + static_cast<int>(rank) * (it.wide / 2), it.wide);
+          }
         }
+        grid_dep_wait();
       }
-      if (p.early == PG_EARLY_B) grid_dep_wait();
-      for (int t = cl; t < items && ok; t += ncl) {
-        int mt, nt, kz, kb0, kb1;
-        item_at(t, mt, nt, kz, kb0, kb1);
-        const int m0 = mt * 256 + static_cast<int>(rank) * 128;
-        const int n0 = nt * p.bn + static_cast<int>(rank) * bh;
-        for (int kb = kb0; kb < kb1; ++kb) {
+      for (int i = 0; ok && item_at(i, it); ++i) {
+        const bool second = TWO && it.job == 1;
+        const PairGemmParams& p = second ? p1 : p0;
+        const CUtensorMap& tm_a = second ? tm_a1 : tm_a0;
+        const CUtensorMap& tm_b = second ? tm_b1 : tm_b0;
+        const bool a_mn = second ? J1::A_MN : J0::A_MN, b_mn = second ? J1::B_MN : J0::B_MN;
+        const uint32_t stage_bytes = bytes_of(it, p, b_mn);
+        const int m0 = it.mt * 256 + static_cast<int>(rank) * 128;
+        const int n0 = it.nt * p.bn + static_cast<int>(rank) * (it.wide / 2);
+        for (int kb = it.kb0; kb < it.kb1; ++kb) {
           if (issued >= ahead) {
             if (!mbar_wait_cluster(&empty[s], ph ^ 1u, abort_flag)) {
               ok = false;
               break;
             }
             if (leader) mbar_arrive_expect_tx(&full[s], 2 * stage_bytes);
-            load_b(s, kb, n0);
+            load_b(b_mn, tm_b, s, kb, n0, it.wide);
           }
-          load_a(s, kb, m0);
+          load_a(a_mn, tm_a, s, kb, m0);
           ++issued;
           if (++s == kPgStages) {
             s = 0;
@@ -284,50 +366,56 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------------ pair MMA issuer (leader)
     if (lane == 0 && leader) {
-      const uint32_t idesc = KIND == PG_I8 ? make_idesc_i8(256, p.bn)
-                                           : make_idesc_bf16(256, p.bn) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
       int s = 0;
       uint32_t ph = 0;
       int acc = 0;
       uint32_t acc_ph = 0;
       bool ok = true;
-      for (int t = cl; t < items && ok; t += ncl) {
-        int mt, nt, kz, kb0, kb1;
-        item_at(t, mt, nt, kz, kb0, kb1);
-        if (!mbar_wait_cluster(&acc_empty[acc], acc_ph ^ 1u, abort_flag)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after_sync();
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 256);
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait_cluster(&full[s], ph, abort_flag)) {
+      PgItem it;
+      for (int i = 0; ok && item_at(i, it); ++i) {
+        const bool second = TWO && it.job == 1;
+        const int kchunk = second ? p1.kchunk : p0.kchunk;
+        const bool a_mn = second ? J1::A_MN : J0::A_MN, b_mn = second ? J1::B_MN : J0::B_MN;
+        const uint32_t idesc = KIND == PG_I8 ? make_idesc_i8(256, it.wide)
+                                             : make_idesc_bf16(256, it.wide) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+        int kb = it.kb0;
+        do {  // one accumulation; a tile without k still hands its (empty) accumulator on
+          const int end = min(kb + kchunk, it.kb1);
+          if (!mbar_wait_cluster(&acc_empty[acc], acc_ph ^ 1u, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after_sync();
-          const uint32_t a_addr = smem_u32(sA + s * kPgTileBytes);
-          const uint32_t b_addr = smem_u32(sB + s * kPgTileBytes);
+          const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 256);
+          for (int first = kb; kb < end; ++kb) {
+            if (!mbar_wait_cluster(&full[s], ph, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after_sync();
+            const uint32_t a_addr = smem_u32(sA + s * kPgTileBytes);
+            const uint32_t b_addr = smem_u32(sB + s * kPgTileBytes);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {  // K-major: 32 bytes of every row; MN-major: 16 lines
-            const uint64_t da = A_MN ? make_sdesc_mn_sw128(a_addr + k * 2048) : make_sdesc_sw128(a_addr + k * 32);
-            const uint64_t db = B_MN ? make_sdesc_mn_sw128(b_addr + k * 2048) : make_sdesc_sw128(b_addr + k * 32);
-            const uint32_t accumulate = (kb != kb0 || k != 0) ? 1u : 0u;
-            if (KIND == PG_I8)
-              tc_mma_i8_pair(d_tmem, da, db, idesc, accumulate);
-            else
-              tc_mma_bf16_pair(d_tmem, da, db, idesc, accumulate);
+            for (int k = 0; k < 4; ++k) {  // K-major: 32 bytes of every row; MN-major: 16 lines
+              const uint64_t da = a_mn ? make_sdesc_mn_sw128(a_addr + k * 2048) : make_sdesc_sw128(a_addr + k * 32);
+              const uint64_t db = b_mn ? make_sdesc_mn_sw128(b_addr + k * 2048) : make_sdesc_sw128(b_addr + k * 32);
+              const uint32_t accumulate = (kb != first || k != 0) ? 1u : 0u;
+              if (KIND == PG_I8)
+                tc_mma_i8_pair(d_tmem, da, db, idesc, accumulate);
+              else
+                tc_mma_bf16_pair(d_tmem, da, db, idesc, accumulate);
+            }
+            tc_commit_pair_mc(&empty[s], 0x3);  // frees stage s in both CTAs once read
+            if (++s == kPgStages) {
+              s = 0;
+              ph ^= 1u;
+            }
           }
-          tc_commit_pair_mc(&empty[s], 0x3);  // frees stage s in both CTAs once read
-          if (++s == kPgStages) {
-            s = 0;
-            ph ^= 1u;
-          }
-        }
-        if (!ok) break;
-        tc_commit_pair_mc(&acc_full[acc], 0x3);
-        acc ^= 1;
-        if (acc == 0) acc_ph ^= 1u;
+          if (!ok) break;
+          tc_commit_pair_mc(&acc_full[acc], 0x3);
+          acc ^= 1;
+          if (acc == 0) acc_ph ^= 1u;
+        } while (kb < it.kb1);
       }
       if (!ok) {
         tc_commit_pair_mc(drain, 0x1);
@@ -341,37 +429,49 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     const int q = warp & 3;
     const uint32_t leader_acc_empty0 = dsmem_addr(&acc_empty[0], 0);
     const uint32_t leader_acc_empty1 = dsmem_addr(&acc_empty[1], 0);
-    int acc = 0, turn = 0;
+    int acc = 0;
     uint32_t acc_ph = 0;
-    for (int t = cl; t < items; t += ncl, ++turn) {
-      int mt, nt, kz, kb0, kb1;
-      item_at(t, mt, nt, kz, kb0, kb1);
+    PgItem it;
+    // One tile: false once a wait gave up.
+    auto finish = [&](auto* job, const PairGemmParams& p, const auto& ep, const PgPlan& pl, int turn) {
+      using Epi = typename std::remove_pointer_t<decltype(job)>::Epi;
       PgTile tile;
-      tile.row0 = mt * 256 + static_cast<int>(rank) * 128 + q * 32;
-      tile.n0 = nt * p.bn;
-      tile.width = min(p.bn, p.N - tile.n0);
+      tile.row0 = it.mt * 256 + static_cast<int>(rank) * 128 + q * 32;
+      tile.n0 = it.nt * p.bn;
+      tile.width = it.width;
       tile.half = (warp - 2) >> 2;
       tile.turn = turn;
-      tile.nt = nt;
-      tile.kz = kz;
-      tile.M = rows;
-      tile.empty = kb0 == kb1;
+      tile.nt = it.nt;
+      tile.kz = it.kz;
+      tile.M = pl.rows;
+      tile.empty = it.kb0 == it.kb1;
+      tile.chunks = max(1, (it.kb1 - it.kb0 + p.kchunk - 1) / p.kchunk);
       tile.stage = sOut + (warp - 2) * kPgOutBytes;
-      tile.t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * 256);
       Epi epi(ep, p, tile, lane);  // row parameters are on their way while the MMAs finish
-      if (!mbar_wait_cluster(&acc_full[acc], acc_ph, abort_flag)) break;
-      tc_fence_after_sync();
-      epi.run(ep, p, tile, lane);
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) {
-        if (leader)
-          mbar_arrive(&acc_empty[acc]);
-        else
-          mbar_arrive_remote(acc == 0 ? leader_acc_empty0 : leader_acc_empty1);
+      for (tile.chunk = 0; tile.chunk < tile.chunks; ++tile.chunk) {
+        tile.t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * 256);
+        if (!mbar_wait_cluster(&acc_full[acc], acc_ph, abort_flag)) return false;
+        tc_fence_after_sync();
+        epi.run(ep, p, tile, lane);
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if (leader)
+            mbar_arrive(&acc_empty[acc]);
+          else
+            mbar_arrive_remote(acc == 0 ? leader_acc_empty0 : leader_acc_empty1);
+        }
+        acc ^= 1;
+        if (acc == 0) acc_ph ^= 1u;
       }
-      acc ^= 1;
-      if (acc == 0) acc_ph ^= 1u;
+      return true;
+    };
+    bool ok = true;
+    for (int i = 0; ok && item_at(i, it); ++i) {
+      if (TWO && it.job == 1)
+        ok = finish(static_cast<J1*>(nullptr), p1, ep1, plan1, i);
+      else
+        ok = finish(static_cast<J0*>(nullptr), p0, ep0, plan0, i);
     }
   }
 
@@ -381,6 +481,24 @@ __global__ void __launch_bounds__(kPgThreads, 1)
   cluster_sync_all();  // no CTA leaves while the other may still signal its barriers
   tc_fence_after_sync();
   if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
+}
+
+template <int KIND, class J>
+__global__ void __launch_bounds__(kPgThreads, 1)
+    k_pair_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                const __grid_constant__ PairGemmParams p, const __grid_constant__ typename J::Params ep) {
+  const PgNoEpi::Params none;
+  pair_gemm_body<KIND, J, PgNoJob, false>(tm_a, tm_b, p, ep, tm_a, tm_b, p, none);
+}
+
+// Two bf16 products in one launch.
+template <class J0, class J1>
+__global__ void __launch_bounds__(kPgThreads, 1)
+    k_pair_gemm2(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_b0,
+                 const __grid_constant__ PairGemmParams p0, const __grid_constant__ typename J0::Params ep0,
+                 const __grid_constant__ CUtensorMap tm_a1, const __grid_constant__ CUtensorMap tm_b1,
+                 const __grid_constant__ PairGemmParams p1, const __grid_constant__ typename J1::Params ep1) {
+  pair_gemm_body<PG_BF16, J0, J1, true>(tm_a0, tm_b0, p0, ep0, tm_a1, tm_b1, p1, ep1);
 }
 
 }  // namespace fn
