@@ -16,6 +16,23 @@ fn_status make_mn_map(CUtensorMap* map, const void* ptr, int64_t cols, int64_t k
   return FN_OK;
 }
 
+// The same as blocks of 64 columns, cols % 64 == 0: boxes of `blocks` blocks x 64 k, one copy per stage (two copies took ...).
+fn_status make_mn_block_map(CUtensorMap* map, const void* ptr, int64_t cols, int64_t k, int64_t ld, int blocks) {
+  cuuint64_t dims[3] = {64u, static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(cols / 64)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, 128u};
+  cuuint32_t box[3] = {64u, 64u, static_cast<cuuint32_t>(blocks)};
+  CUresult r = encode_cached(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box,
+                             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+  if (r == CUDA_ERROR_NOT_FOUND) return fail(FN_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  if (r != CUDA_SUCCESS) return fail(FN_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
+  return FN_OK;
+}
+
+fn_status make_mn_operand(CUtensorMap* map, fn::PairGemmParams* p, const void* ptr, int64_t cols, int64_t k) {
+  p->b_blocks = cols % 64 == 0;
+  return p->b_blocks ? make_mn_block_map(map, ptr, cols, k, cols, p->bn / 128) : make_mn_map(map, ptr, cols, k, cols);
+}
+
 // 2-D bf16 K-major operand [rows][k] with row stride ld: 64 k x box_rows boxes, 128-byte swizzle.
 fn_status make_k_map(CUtensorMap* map, const void* ptr, int64_t k, int64_t rows, int64_t ld, int box_rows) {
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
@@ -28,6 +45,9 @@ fn_status make_k_map(CUtensorMap* map, const void* ptr, int64_t k, int64_t rows,
   return FN_OK;
 }
 
+// Masks of 32 live rows, whole row tiles of the logits' product.
+int64_t ce_ld_hits(int64_t M) { return round_up(M, 256) / 32; }
+
 // What a call works through and where the parts of its workspace start.
 struct CePlan {
   int64_t piece;   // vocabulary columns of a piece (forward: all)
@@ -35,7 +55,7 @@ struct CePlan {
   int n_tiles;     // column tiles of a full piece
   int ksplit;      // K ranges of dx's product
   int64_t rstd, part, tlogit;                        // forward
-  int64_t n_live, rows, rank_of, target, u, xc, P, acc, bytes;  // backward (and part)
+  int64_t n_live, rows, rank_of, target, u, hits, xc, P, acc, bytes;  // backward (and part)
 };
 
 // Stages per accumulation of the forward's logits: 1024 k keep the drift of the tensor core's sums near 1e-6.
@@ -55,6 +75,8 @@ int ce_dx_ksplit(const fn::PairGemmParams& dx, const fn::PairGemmParams& dw, int
   return k;
 }
 
+constexpr int kCeFwdParts = fn::CeFwdEpi<false>::kParts;
+
 constexpr int64_t kCePieceBytes = int64_t{64} << 20;  // of P, per piece
 
 CePlan ce_plan(int64_t M, int64_t d, int64_t V, bool backward, int sms) {
@@ -72,7 +94,7 @@ CePlan ce_plan(int64_t M, int64_t d, int64_t V, bool backward, int sms) {
   if (!backward) {
     c.rstd = 0;
     c.part = round_up(4 * M, 256);
-    c.tlogit = c.part + round_up(16ll * c.n_tiles * M, 256);
+    c.tlogit = c.part + round_up(8ll * kCeFwdParts * c.n_tiles * M, 256);
     c.bytes = c.tlogit + round_up(4 * M, 256);
     return c;
   }
@@ -86,8 +108,9 @@ CePlan ce_plan(int64_t M, int64_t d, int64_t V, bool backward, int sms) {
   c.rank_of = c.rows + round_up(16 * M, 256);
   c.target = c.rank_of + round_up(4 * M, 256);
   c.u = c.target + round_up(4 * M, 256);
-  c.part = c.u + round_up(4 * M, 256);
-  c.xc = c.part + round_up(8ll * c.n_tiles * c.pieces * M, 256);
+  c.hits = c.u + round_up(4 * M, 256);
+  c.part = c.hits + round_up(4 * ((c.piece + 31) / 32) * ce_ld_hits(M), 256);
+  c.xc = c.part + round_up(4ll * fn::CeGradEpi::kParts * c.n_tiles * c.pieces * M, 256);
   c.P = c.xc + round_up(2 * Mp * d, 256);
   c.acc = c.P + 2 * Mp * round_up(c.piece, 64);
   c.bytes = c.acc + 4 * c.ksplit * M * d;
@@ -174,7 +197,7 @@ fn_status flashnorm_linear_cross_entropy(const void* x, const void* Wstar, const
   if (st != FN_OK) return st;
   cudaError_t e = launch_kernel(fn::k_ce_join, dim3(static_cast<unsigned>((M + 7) / 8)), dim3(256), 0, s, 1,
                                 static_cast<const float2*>(ep.part), static_cast<const float*>(ep.tlogit), ep.targets,
-                                static_cast<float*>(loss), static_cast<float*>(lse), p.M, p.N, 2 * p.num_n_tiles,
+                                static_cast<float*>(loss), static_cast<float*>(lse), p.M, p.N, kCeFwdParts * p.num_n_tiles,
                                 static_cast<long long>(ignore_index));
   return e == cudaSuccess ? FN_OK : cuda_fail(e, "cross entropy join launch");
 }
@@ -206,7 +229,8 @@ fn_status flashnorm_linear_cross_entropy_backward(const void* g, const void* x, 
   fn::CeRow* rows = reinterpret_cast<fn::CeRow*>(base + c.rows);
   int* rank_of = reinterpret_cast<int*>(base + c.rank_of);
   uint16_t* xc = reinterpret_cast<uint16_t*>(base + c.xc);
-  const fn::CeLive live = {n_live, reinterpret_cast<int*>(base + c.target), reinterpret_cast<float*>(base + c.u)};
+  const fn::CeLive live = {n_live, reinterpret_cast<int*>(base + c.target), reinterpret_cast<float*>(base + c.u),
+                          reinterpret_cast<unsigned*>(base + c.hits), static_cast<int>(ce_ld_hits(M))};
   float* cpart = reinterpret_cast<float*>(base + c.part);
   uint16_t* P = reinterpret_cast<uint16_t*>(base + c.P);
   float* acc = reinterpret_cast<float*>(base + c.acc);
@@ -230,8 +254,8 @@ fn_status flashnorm_linear_cross_entropy_backward(const void* g, const void* x, 
     p.N = static_cast<int>(width);
     p.num_n_tiles = static_cast<int>((width + p.bn - 1) / p.bn);
     p.live = n_live;
-    const fn::CeGradParams ge = {rows, P, cpart + static_cast<int64_t>(parts) * M, static_cast<int>(ldp), static_cast<int>(v0), live.u};
-    parts += 2 * p.num_n_tiles;
+    const fn::CeGradParams ge = {rows, P, cpart + static_cast<int64_t>(parts) * M, static_cast<int>(ldp), static_cast<int>(v0), live};
+    parts += fn::CeGradEpi::kParts * p.num_n_tiles;
     if ((st = make_k_map(&ta, xc, d, Mp, d, 128)) != FN_OK) return st;
     if ((st = make_k_map(&tb, W, d, width, d, p.bn / 2)) != FN_OK) return st;
     if ((st = launch_pair_gemm<fn::PG_BF16, fn::PgJob<false, false, fn::CeGradEpi>>(ta, tb, p, ge, sms, dev, s, "cross entropy P")) != FN_OK)
@@ -241,14 +265,14 @@ fn_status flashnorm_linear_cross_entropy_backward(const void* g, const void* x, 
     p.live = n_live;
     const fn::CeDxParams xe = {acc, static_cast<int>(d), v0 > 0};
     if ((st = make_k_map(&ta, P, width, Mp, ldp, 128)) != FN_OK) return st;
-    if ((st = make_mn_map(&tb, W, d, width, d)) != FN_OK) return st;
+    if ((st = make_mn_operand(&tb, &p, W, d, width)) != FN_OK) return st;
     plan_pair_gemm_bn(&q, width, d, (M + 63) / 64, ce_mn_width(d), 1);
     q.live = n_live;
     q.live_is_k = 1;
     q.extra = std::max(1, p.num_kb / p.ksplit / q.num_kb);
     const fn::CeDwParams we = {live, xc, static_cast<uint16_t*>(dWstar) + v0 * d, static_cast<int>(d), static_cast<int>(v0)};
-    if ((st = make_mn_map(&ta1, P, width, Mp, ldp)) != FN_OK) return st;
-    if ((st = make_mn_map(&tb1, xc, d, Mp, d)) != FN_OK) return st;
+    if ((st = make_mn_block_map(&ta1, P, ldp, Mp, ldp, 2)) != FN_OK) return st;
+    if ((st = make_mn_operand(&tb1, &q, xc, d, Mp)) != FN_OK) return st;
     st = launch_pair_gemm2<fn::PgJob<false, true, fn::CeDxEpi>, fn::PgJob<true, true, fn::CeDwEpi>>(
         ta, tb, p, xe, ta1, tb1, q, we, sms, dev, s, "cross entropy gradients");
     if (st != FN_OK) return st;

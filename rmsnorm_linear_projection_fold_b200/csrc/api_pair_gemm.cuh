@@ -25,9 +25,9 @@ void plan_pair_gemm(fn::PairGemmParams* p, int64_t M, int64_t N, int64_t num_kb,
 int64_t pair_items(const fn::PairGemmParams& p) { return static_cast<int64_t>(p.num_m_tiles) * p.num_n_tiles * p.ksplit; }
 
 template <typename Kern>
-fn_status configure_pair_gemm(Kern kern, bool* configured, const char* what) {
+fn_status configure_pair_gemm(Kern kern, int parts, bool* configured, const char* what) {
   if (*configured) return FN_OK;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, fn::pair_gemm_smem_bytes());
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, fn::pair_gemm_smem_bytes(parts));
   if (e != cudaSuccess) return cuda_fail(e, what);
   *configured = true;
   return FN_OK;
@@ -37,14 +37,15 @@ template <int KIND, class J>
 fn_status launch_pair_gemm(const CUtensorMap& ta, const CUtensorMap& tb, const fn::PairGemmParams& p,
                            const typename J::Params& ep, int sms, int dev, cudaStream_t s, const char* what) {
   auto kern = fn::k_pair_gemm<KIND, J>;
+  constexpr int parts = J::Epi::kParts;
   static bool configured[kMaxDevices] = {false};
-  fn_status st = configure_pair_gemm(kern, &configured[dev], what);
+  fn_status st = configure_pair_gemm(kern, parts, &configured[dev], what);
   if (st != FN_OK) return st;
   const int64_t items = pair_items(p);
   if (items > kMaxDim) return fail(FN_ERR_UNSUPPORTED, "%s: too many tiles", what);
   const int pairs = static_cast<int>(std::min<int64_t>(items, sms / 2));
-  cudaError_t e = launch_kernel(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(fn::kPgThreads),
-                                fn::pair_gemm_smem_bytes(), s, 2, ta, tb, p, ep);
+  cudaError_t e = launch_kernel(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(fn::pair_gemm_threads(parts)),
+                                fn::pair_gemm_smem_bytes(parts), s, 2, ta, tb, p, ep);
   return e == cudaSuccess ? FN_OK : cuda_fail(e, what);
 }
 
@@ -54,14 +55,15 @@ fn_status launch_pair_gemm2(const CUtensorMap& ta0, const CUtensorMap& tb0, cons
                             const fn::PairGemmParams& p1, const typename J1::Params& ep1, int sms, int dev,
                             cudaStream_t s, const char* what) {
   auto kern = fn::k_pair_gemm2<J0, J1>;
+  constexpr int parts = J0::Epi::kParts;
   static bool configured[kMaxDevices] = {false};
-  fn_status st = configure_pair_gemm(kern, &configured[dev], what);
+  fn_status st = configure_pair_gemm(kern, parts, &configured[dev], what);
   if (st != FN_OK) return st;
   const int64_t items = pair_items(p0) + pair_items(p1);
   if (items > kMaxDim) return fail(FN_ERR_UNSUPPORTED, "%s: too many tiles", what);
   const int pairs = static_cast<int>(std::min<int64_t>(items, sms / 2));
-  cudaError_t e = launch_kernel(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(fn::kPgThreads),
-                                fn::pair_gemm_smem_bytes(), s, 2, ta0, tb0, p0, ep0, ta1, tb1, p1, ep1);
+  cudaError_t e = launch_kernel(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(fn::pair_gemm_threads(parts)),
+                                fn::pair_gemm_smem_bytes(parts), s, 2, ta0, tb0, p0, ep0, ta1, tb1, p1, ep1);
   return e == cudaSuccess ? FN_OK : cuda_fail(e, what);
 }
 

@@ -5,7 +5,7 @@
 // Normalization for Transformers", Abstract): with r[m] = 1/sqrt(mean(x[m]^2) + eps),
 //     l[m, n] = r[m] sum_k x[m, k] W*[n, k],   lse[m] = log sum_n exp(l[m, n]),   loss[m] = lse[m] - l[m, t[m]].
 // Forward: the logits of a 256-row tile exist only in tensor memory; each epilogue thread owns a row and keeps the
-// running maximum and sum of exponentials of its columns, one (max, sum) pair per row, column tile and warp half goes
+// running maximum and sum of exponentials of its columns, one (max, sum) pair per row, column tile and warp goes
 // to the workspace, and a second kernel joins them in a fixed order.
 // Backward: rows without a target have no gradient, so the live rows are packed first and only they go through the three
 // products (a batch half of prompt or padding costs half; what such rows hold cannot reach dW*). Then, in pieces of the
@@ -66,18 +66,20 @@ __device__ __forceinline__ bool target_is_class(long long t, int V) { return t >
 struct CeFwdParams {
   const float* rstd;
   const long long* targets;
-  float2* part;   // [M][2 column tiles]: running maximum (of log2 e times the logits) and sum of 2^(. - max)
+  float2* part;   // [M][kParts column tiles]: running maximum (of log2 e times the logits) and sum of 2^(. - max)
   float* tlogit;  // [M] logit of the target
 };
 
-// A thread's columns of a tile are up to four chunks of 32, alternating with the quarter's other warp. HELD: the tile takes
+// A thread's columns of a tile are up to kChunks chunks of 32, shared out among the quarter's warps. HELD: the tile takes
 // several accumulations, whose sums so far stay in registers.
 template <bool HELD>
 struct CeFwdEpi {
+  static constexpr int kParts = 4;
+  static constexpr int kChunks = 8 / kParts;
   using Params = CeFwdParams;
   float rstd, r2;  // r2 = r log2(e): the exponentials are powers of two
   long long tgt;
-  float held[HELD ? 4 : 1][32];
+  float held[HELD ? kChunks : 1][32];
   __device__ __forceinline__ CeFwdEpi(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
     const int row = t.row0 + lane;
     rstd = row < t.M ? __ldcg(e.rstd + row) : 0.f;
@@ -85,67 +87,71 @@ struct CeFwdEpi {
     tgt = row < t.M ? __ldg(e.targets + row) : -1;
     if (HELD) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < kChunks; ++i)
 #pragma unroll
         for (int j = 0; j < 32; ++j) held[HELD ? i : 0][j] = 0.f;
     }
   }
   __device__ __forceinline__ void run(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
     const int row = t.row0 + lane;
-    const int c00 = 32 * ((t.half + t.turn) & 1);
+    const int c00 = 32 * t.part;
     float m = -INFINITY, s = 0.f;
-    auto load = [&](int c0, uint32_t (&v)[2][16]) {
-      tmem_ld16(t.t_row + c0, v[0]);
-      tmem_ld16(t.t_row + c0 + 16, v[1]);
-      tmem_ld_wait();
-      reg_fence16(v[0]);
-      reg_fence16(v[1]);
-    };
     if (HELD && t.chunk < t.chunks - 1) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kChunks; ++i) {
         uint32_t v[2][16];
-        if (c00 + 64 * i >= t.width) continue;
-        load(c00 + 64 * i, v);
+        if (c00 + 32 * kParts * i >= t.width) continue;
+        tmem_ld16(t.t_row + c00 + 32 * kParts * i, v[0]);
+        tmem_ld16(t.t_row + c00 + 32 * kParts * i + 16, v[1]);
+        tmem_ld_wait();
+        reg_fence16(v[0]);
+        reg_fence16(v[1]);
 #pragma unroll
         for (int j = 0; j < 32; ++j) held[HELD ? i : 0][j] += __uint_as_float(v[j >> 4][j & 15]);
       }
       return;
     }
-#pragma unroll(HELD ? 4 : 1)
-    for (int i = 0; i < 4; ++i) {
-      const int c0 = c00 + 64 * i;
+    // with sums held, 16 columns at a time, which saves registers
+    constexpr int kCols = HELD ? 16 : 32;
+#pragma unroll(HELD ? kChunks * 2 : 1)
+    for (int i = 0; i < kChunks * 32 / kCols; ++i) {
+      const int c0 = c00 + 32 * kParts * (i * kCols / 32) + i * kCols % 32;
       if (c0 >= t.width) break;
-      float z[32];
+      float z[kCols];
       {
-        uint32_t v[2][16];
-        load(c0, v);
+        uint32_t v[kCols / 16][16];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) z[j] = (HELD ? held[HELD ? i : 0][j] : 0.f) + __uint_as_float(v[j >> 4][j & 15]);
+        for (int b = 0; b < kCols / 16; ++b) tmem_ld16(t.t_row + c0 + 16 * b, v[b]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int b = 0; b < kCols / 16; ++b) reg_fence16(v[b]);
+#pragma unroll
+        for (int j = 0; j < kCols; ++j)
+          z[j] = (HELD ? held[HELD ? i * kCols / 32 : 0][HELD ? i * kCols % 32 + j : 0] : 0.f) + __uint_as_float(v[j >> 4][j & 15]);
       }
       const long long at = tgt - (t.n0 + c0);
-      if (at >= 0 && at < 32) {
+      if (at >= 0 && at < kCols) {
         float lt = 0.f;
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
+        for (int j = 0; j < kCols; ++j)
           if (at == j) lt = z[j];
         if (c0 + at < t.width) e.tlogit[row] = lt * rstd;
       }
-      const bool edge = c0 + 32 > t.width;  // columns past the vocabulary take no part
+      const bool edge = c0 + kCols > t.width;  // columns past the vocabulary take no part
       if (edge) {
 #pragma unroll
-        for (int j = 1; j < 32; ++j)
+        for (int j = 1; j < kCols; ++j)
           if (c0 + j >= t.width) z[j] = z[0];
       }
       float mc = z[0];
 #pragma unroll
-      for (int j = 1; j < 32; ++j) mc = fmaxf(mc, z[j]);
+      for (int j = 1; j < kCols; ++j) mc = fmaxf(mc, z[j]);
       const float mn = fmaxf(m, mc * r2);
       const float base = mn == -INFINITY ? 0.f : mn;  // a row of -inf so far: 2^(-inf) = 0, not NaN
       const uint64_t rr = pack_f32x2(r2, r2), nb = pack_f32x2(-base, -base);
       uint64_t a0 = 0, a1 = 0;
 #pragma unroll
-      for (int j = 0; j < 32; j += 4) {
+      for (int j = 0; j < kCols; j += 4) {
         const float2 q0 = unpack_f32x2(fma_f32x2(pack_f32x2(z[j], z[j + 1]), rr, nb));
         const float2 q1 = unpack_f32x2(fma_f32x2(pack_f32x2(z[j + 2], z[j + 3]), rr, nb));
         float e0 = ex2(q0.x), e1 = ex2(q0.y), e2 = ex2(q1.x), e3 = ex2(q1.y);
@@ -163,7 +169,7 @@ struct CeFwdEpi {
       m = mn;
     }
     if (row < t.M)
-      e.part[static_cast<size_t>(row) * (2 * p.num_n_tiles) + 2 * t.nt + t.half] = make_float2(m, s);
+      e.part[static_cast<size_t>(row) * (kParts * p.num_n_tiles) + kParts * t.nt + t.part] = make_float2(m, s);
   }
 };
 
@@ -219,6 +225,9 @@ struct CeLive {
   const int* n_live;
   int* target;  // [live rows]
   float* u;     // r dl of the target's entry
+  // [32 vocabulary columns of the piece][ld_hits: 32 live rows]: which of these rows have their target among these columns
+  unsigned* hits;
+  int ld_hits;
 };
 
 constexpr int kCeIgnored = -1, kCeBad = -2;  // in place of a row's rank among the live ones
@@ -323,13 +332,14 @@ __global__ void __launch_bounds__(256) k_ce_pack(const uint16_t* __restrict__ x,
 struct CeGradParams {
   const CeRow* rows;
   uint16_t* P;     // bf16 [live rows, and up to the next multiple of 64][ldp], this piece's columns
-  float* cpart;    // [2 column tiles][M] partial c, this piece's
+  float* cpart;    // [kParts column tiles][M] partial c, this piece's
   int ldp;         // a multiple of 64: rows of P start on whole 128-byte lines
   int v0;          // first column of the piece within the vocabulary
-  float* u;        // CeLive's
+  CeLive live;
 };
 
 struct CeGradEpi {
+  static constexpr int kParts = 2;
   using Params = CeGradParams;
   CeRow q;
   __device__ __forceinline__ CeGradEpi(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
@@ -349,7 +359,7 @@ struct CeGradEpi {
     uint64_t c2 = 0;  // sum of exp(l - lse) z; c = g r times it
     float ct = 0.f;   // the target's -z
     const int t0 = q.target - (e.v0 + t.n0);  // the target's column in this tile, if it has it
-    for (int ch = (t.half + t.turn) & 1; ch * 32 < t.width; ch += 2) {
+    for (int ch = t.part; ch * 32 < t.width; ch += kParts) {
       const int c0 = ch * 32;
       uint32_t v[2][16];
       tmem_ld16(t.t_row + c0, v[0]);
@@ -381,7 +391,10 @@ struct CeGradEpi {
           }
       }
       const int at = t0 - c0;
-      if (row < t.M && at >= 0 && at < 32 && c0 + at < t.width) {  // the target's entry: kept in fp32, 0 in P
+      const bool hit = row < t.M && at >= 0 && at < 32 && c0 + at < t.width;
+      const unsigned hits = __ballot_sync(0xffffffffu, hit);
+      if (lane == 0) e.live.hits[static_cast<size_t>((t.n0 + c0) >> 5) * e.live.ld_hits + (t.row0 >> 5)] = hits;
+      if (hit) {  // the target's entry: kept in fp32, 0 in P
         float z = 0.f;
 #pragma unroll
         for (int j = 0; j < 32; ++j)
@@ -389,7 +402,7 @@ struct CeGradEpi {
             z = __uint_as_float(v[j >> 4][j & 15]);
             if (j & 1) o[j >> 1].y = 0.f; else o[j >> 1].x = 0.f;
           }
-        e.u[row] = gr * (ex2(fmaf(z, r2, q.nlse2)) - 1.0f);
+        e.live.u[row] = gr * (ex2(fmaf(z, r2, q.nlse2)) - 1.0f);
         ct = -z;
       }
 #pragma unroll
@@ -400,15 +413,15 @@ struct CeGradEpi {
       pg_flush(t.stage, lane, e.P, static_cast<size_t>(e.ldp) * 2, t.row0, (t.M + 63) & ~63, 2ll * (t.n0 + c0), 2ll * e.ldp);
     }
     const float2 cs = unpack_f32x2(c2);
-    if (row < t.M) e.cpart[static_cast<size_t>(2 * t.nt + t.half) * p.M + row] = gr * ((cs.x + cs.y) + ct);
+    if (row < t.M) e.cpart[static_cast<size_t>(kParts * t.nt + t.part) * p.M + row] = gr * ((cs.x + cs.y) + ct);
   }
 };
 
 // dW*: the product plus the target entries' share, rounded to bf16 once. Of a warp's 32 vocabulary rows few are a target:
-// while the MMAs run it looks through the live rows' targets (two loads of 32 per stage of K, sixteen in flight) and lists
-// those it finds, lane k the k-th. The rows found are added in their order, eight at a time: the lanes load the chunk's 32
-// columns of u x (for the first eight one chunk ahead) and pass them through the staging buffer to the lane whose row it
-// is. A warp with more than 32 hits (a frequent token) looks for the further ones again in every chunk.
+// while the MMAs run it lists the live rows that have one of them (from the masks that P's epilogue left, 4 bytes per 32
+// live rows), lane k the k-th. They are added in their order, eight at a time: the lanes load the chunk's 32 columns of
+// u x (for the first eight one chunk ahead) and pass them through the staging buffer to the lane whose row it is. A warp
+// with more than 32 hits (a frequent token) lists the further ones again in every chunk.
 struct CeDwParams {
   CeLive live;
   const uint16_t* xc;  // [live rows][ldy]
@@ -424,43 +437,43 @@ struct CeDwHits {
   float u;
 };
 struct CeDwEpi {
+  static constexpr int kParts = 2;
   using Params = CeDwParams;
   int base, live;  // first vocabulary row of the warp; live rows
+  int slab;        // the warp's row of the masks
   CeDwHits first;
   float val[8];  // of the first eight hits, for the chunk to come
 
   __device__ __forceinline__ CeDwHits look(const Params& e, int from, int lane) const {
     CeDwHits h = {0, live, 0, 0, 0.f};
-    for (int r0 = from & ~31; r0 < live; r0 += 512) {
-      int t[16];
+    const unsigned* masks = e.live.hits + static_cast<size_t>(slab) * e.live.ld_hits;
+    const int words = (live + 31) >> 5;
+    for (int g0 = from >> 5; g0 < words; g0 += 128) {
+      unsigned w[4];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int r = r0 + 32 * i + lane;
-        t[i] = r >= from && r < live ? __ldcg(e.live.target + r) - base : -1;
-      }
-      bool any = false;
+      for (int i = 0; i < 4; ++i) w[i] = g0 + 32 * i + lane < words ? __ldcg(masks + g0 + 32 * i + lane) : 0u;
+      if (lane == 0 && g0 == from >> 5) w[0] &= 0xffffffffu << (from & 31);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) any |= static_cast<unsigned>(t[i]) < 32u;
-      if (!__any_sync(0xffffffffu, any)) continue;
-#pragma unroll 1
-      for (int i = 0; i < 16; ++i) {
-        int ti = t[0];
-#pragma unroll
-        for (int k = 0; k < 15; ++k) t[k] = t[k + 1];
-        unsigned hits = __ballot_sync(0xffffffffu, static_cast<unsigned>(ti) < 32u);
-        for (; hits != 0; hits &= hits - 1) {
-          const int src = __ffs(hits) - 1, row = __shfl_sync(0xffffffffu, ti, src);
-          if (h.n == 32) {
-            h.next = r0 + 32 * i + src;
-            goto done;
+      for (int i = 0; i < 4; ++i) {
+        for (unsigned some = __ballot_sync(0xffffffffu, w[i] != 0); some != 0; some &= some - 1) {
+          const int src = __ffs(some) - 1;
+          for (unsigned hits = __shfl_sync(0xffffffffu, w[i], src); hits != 0; hits &= hits - 1) {
+            const int r = 32 * (g0 + 32 * i + src) + __ffs(hits) - 1;
+            if (h.n == 32) {
+              h.next = r;
+              goto done;
+            }
+            if (lane == h.n) h.r = r;
+            ++h.n;
           }
-          if (lane == h.n) h.r = r0 + 32 * i + src, h.row = row;
-          ++h.n;
         }
       }
     }
   done:
-    if (lane < h.n) h.u = __ldcg(e.live.u + h.r);
+    if (lane < h.n) {
+      h.row = __ldcg(e.live.target + h.r) - base;
+      h.u = __ldcg(e.live.u + h.r);
+    }
     return h;
   }
   // u x of hits k0 .. k0+7 at the lane's column
@@ -499,19 +512,20 @@ struct CeDwEpi {
 
   __device__ __forceinline__ CeDwEpi(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
     base = e.v0 + t.row0;
-    live = __ldcg(e.live.n_live);
+    slab = t.row0 >> 5;
+    live = t.row0 < t.M ? __ldcg(e.live.n_live) : 0;
     first = look(e, 0, lane);
-    if (first.n > 0) fetch(e, first, 0, t.n0 + 32 * ((t.half + t.turn) & 1) + lane, p.N);
+    if (first.n > 0) fetch(e, first, 0, t.n0 + 32 * t.part + lane, p.N);
   }
   __device__ __forceinline__ void run(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
-    for (int ch = (t.half + t.turn) & 1; ch * 32 < t.width; ch += 2) {
+    for (int ch = t.part; ch * 32 < t.width; ch += kParts) {
       uint32_t v[2][16];
       tmem_ld16(t.t_row + ch * 32, v[0]);
       tmem_ld16(t.t_row + ch * 32 + 16, v[1]);
       const int col = t.n0 + ch * 32 + lane;
       if (first.n > 0) {
         stage(t, lane);
-        if (first.n <= 8) fetch(e, first, 0, col + 64, p.N);
+        if (first.n <= 8) fetch(e, first, 0, col + 32 * kParts, p.N);
       }
       tmem_ld_wait();
       reg_fence16(v[0]);
@@ -536,7 +550,7 @@ struct CeDwEpi {
           }
           from = h.next;
         }
-        if (first.n > 8) fetch(e, first, 0, col + 64, p.N);
+        if (first.n > 8) fetch(e, first, 0, col + 32 * kParts, p.N);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -559,11 +573,12 @@ struct CeDxParams {
   int add;
 };
 struct CeDxEpi {
+  static constexpr int kParts = 2;
   using Params = CeDxParams;
   __device__ __forceinline__ CeDxEpi(const Params&, const PairGemmParams&, const PgTile&, int) {}
   __device__ __forceinline__ void run(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
     float* plane = e.acc + static_cast<size_t>(t.kz) * p.M * e.ld;
-    for (int ch = (t.half + t.turn) & 1; ch * 16 < t.width; ch += 2) {
+    for (int ch = t.part; ch * 16 < t.width; ch += kParts) {
       uint32_t v[16];
       tmem_ld16(t.t_row + ch * 16, v);
       tmem_ld_wait();

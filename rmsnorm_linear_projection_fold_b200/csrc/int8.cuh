@@ -212,6 +212,7 @@ struct Int8EpiParams {
 // y = rho s acc, or for GLU silu(rho s_g acc_g) (rho s_u acc_u) with gate and up interleaved in blocks of 16 columns.
 template <bool GLU, bool OUT_F32>
 struct Int8Epi {
+  static constexpr int kParts = 2;
   using Params = Int8EpiParams;
   float rho;
   __device__ __forceinline__ Int8Epi(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
@@ -221,7 +222,7 @@ struct Int8Epi {
     constexpr int kOut = OUT_F32 ? 16 : 32;      // outputs of a staged block (64 bytes of a row)
     constexpr int kAcc = GLU ? 2 * kOut : kOut;  // its accumulator columns
     constexpr int kEsz = OUT_F32 ? 4 : 2;
-    for (int ch = (t.half + t.turn) & 1; ch * kAcc < t.width; ch += 2) {
+    for (int ch = t.part; ch * kAcc < t.width; ch += kParts) {
       const int c0 = ch * kAcc;
       uint32_t v[kAcc / 16][16];
 #pragma unroll

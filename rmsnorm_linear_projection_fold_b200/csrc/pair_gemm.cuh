@@ -23,7 +23,9 @@
 // k = 4096 a logit's relative error is near 4e-6). An epilogue that needs better takes the sum in chunks of `kchunk` stages,
 // which it adds in its own registers.
 //
-// Warps: 0 = TMA producer, 1 = MMA issuer (leader) and tensor memory, 2..9 = epilogue, two per lane quarter.
+// Warps: 0 = TMA producer, 1 = MMA issuer (leader) and tensor memory, the others epilogue, Epi::kParts (2 or 4) per lane
+// quarter. Four hide an epilogue's latencies better where a tile is short (the head's P at k = 576: ... us with two) and
+// leave each thread 112 registers instead of 168.
 #pragma once
 
 #include <type_traits>
@@ -34,11 +36,11 @@ namespace fn {
 
 constexpr int kPgStages = 6;
 constexpr int kPgTileBytes = 16 * 1024;  // A or B of one stage: 128 rows x 128 bytes
-constexpr int kPgThreads = 320;
 constexpr int kPgOutBytes = 32 * 64;     // per epilogue warp: 32 rows x 64 bytes on their way out
 
-__host__ __device__ constexpr int pair_gemm_smem_bytes() {
-  return 1024 + kPgStages * 2 * kPgTileBytes + 8 * kPgOutBytes + 1024;
+__host__ __device__ constexpr int pair_gemm_threads(int parts) { return 64 + 128 * parts; }
+__host__ __device__ constexpr int pair_gemm_smem_bytes(int parts) {
+  return 1024 + kPgStages * 2 * kPgTileBytes + 4 * parts * kPgOutBytes + 1024;
 }
 
 struct PairGemmParams {
@@ -53,6 +55,7 @@ struct PairGemmParams {
   int early;        // PgEarly: operands that do not depend on the previous kernel of the stream
   int live_is_k;    // what *live counts: rows of C, or (1) k
   const int* live;  // null, or a count on the device that replaces M (at most M) or num_kb (at most so many stages)
+  int b_blocks;     // MN-major B: its map has blocks of 64 columns as a third dimension, one copy per stage
   int extra;        // job 1: items that a pair with one item less of job 0 takes first, in exchange
 };
 
@@ -95,8 +98,7 @@ struct PgTile {
   uint32_t t_row;  // tensor-memory address of this warp's lanes, accumulator column 0
   int row0;        // first row of the warp's lane quarter
   int n0, width;   // the tile's columns
-  int half;        // which of the quarter's two warps
-  int turn;        // tile counter of this pair: the warps swap chunks from tile to tile
+  int part;        // chunks part, part + kParts, ... of the tile are this warp's (the quarter's warps trade from tile to tile)
   int nt, kz;      // column tile and K range
   int M;           // rows of C
   bool empty;      // no k at all: the accumulator holds nothing and counts as zero
@@ -135,6 +137,7 @@ struct PgJob {
 
 // The empty second job.
 struct PgNoEpi {
+  static constexpr int kParts = 2;
   struct Params {};
   __device__ __forceinline__ PgNoEpi(const Params&, const PairGemmParams&, const PgTile&, int) {}
   __device__ __forceinline__ void run(const Params&, const PairGemmParams&, const PgTile&, int) {}
@@ -160,7 +163,30 @@ struct PgPlan {
 };
 
 struct PgItem {
-  int job, mt, nt, kz, kb0, kb1, width, wide;  // width: columns; wide: the MMA's N
+  int job, mt, nt, kz, kb0, kb1, width, wide;  // job -1: no more; width: columns; wide: the MMA's N
+};
+
+// A warp's walk through its pair's items. Placing one takes a few integer divisions, over 500 cycles in one thread and
+// more than a short tile's MMAs leave between two tiles, so the lanes place the next 32 items at once.
+template <class Place>
+struct PgWalk {
+  const Place& place;  // place(i, item): item i of the pair
+  PgItem mine;
+  int lane, i = 0;
+  __device__ __forceinline__ PgWalk(const Place& p, int l) : place(p), lane(l) {}
+  __device__ __forceinline__ bool next(PgItem& it) {
+    if ((i & 31) == 0) place(i + lane, mine);
+    const int src = i++ & 31;
+    it.job = __shfl_sync(0xffffffffu, mine.job, src);
+    it.mt = __shfl_sync(0xffffffffu, mine.mt, src);
+    it.nt = __shfl_sync(0xffffffffu, mine.nt, src);
+    it.kz = __shfl_sync(0xffffffffu, mine.kz, src);
+    it.kb0 = __shfl_sync(0xffffffffu, mine.kb0, src);
+    it.kb1 = __shfl_sync(0xffffffffu, mine.kb1, src);
+    it.width = __shfl_sync(0xffffffffu, mine.width, src);
+    it.wide = __shfl_sync(0xffffffffu, mine.wide, src);
+    return it.job >= 0;
+  }
 };
 
 template <int KIND, class J0, class J1, bool TWO>
@@ -171,6 +197,8 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tm_a0, const C
   static_assert(KIND == PG_BF16 || (!J0::A_MN && !J0::B_MN && !TWO), "8-bit operands are K-major");
   constexpr int kElem = KIND == PG_I8 ? 1 : 2;
   constexpr int kK = 128 / kElem;  // k per stage
+  constexpr int kParts = J0::Epi::kParts;
+  static_assert(!TWO || J0::Epi::kParts == J1::Epi::kParts, "one set of epilogue warps");
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -178,7 +206,7 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tm_a0, const C
   uint8_t* sA = smem;
   uint8_t* sB = sA + kPgStages * kPgTileBytes;
   uint8_t* sOut = sB + kPgStages * kPgTileBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sOut + 8 * kPgOutBytes);  // used in the leader
+  uint64_t* full = reinterpret_cast<uint64_t*>(sOut + 4 * kParts * kPgOutBytes);  // used in the leader
   uint64_t* empty = full + kPgStages;
   uint64_t* acc_full = empty + kPgStages;  // [2]
   uint64_t* acc_empty = acc_full + 2;      // [2], used in the leader
@@ -198,7 +226,7 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tm_a0, const C
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 16);  // eight epilogue warps of each CTA
+      mbar_init(&acc_empty[b], 8 * kParts);  // the epilogue warps of both CTAs
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -249,85 +277,96 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tm_a0, const C
   const int lights = heavy ? ncl - heavy : 0;
   const int light_extra = TWO && lights ? min(p1.extra, plan1.items / lights) : 0;
   auto item_at = [&](int i, PgItem& it) {
+    it = {-1, 0, 0, 0, 0, 0, 0, 0};
     if (!TWO || i < n0) {
-      const int t = cl + i * ncl;
-      if (t >= plan0.items) return false;
+      const long long t = cl + static_cast<long long>(i) * ncl;  // the lanes look past the last item
+      if (t >= plan0.items) return;
       it.job = 0;
-      place(p0, plan0, J0::B_MN, t, it);
-      return true;
+      place(p0, plan0, J0::B_MN, static_cast<int>(t), it);
+      return;
     }
-    int j = i - max(n0, 0);
-    int t;
+    const int j = i - n0;
+    long long t;
     if (heavy && cl >= heavy) {
-      t = j < light_extra ? (cl - heavy) + j * lights : lights * light_extra + cl + (j - light_extra) * ncl;
+      t = j < light_extra ? (cl - heavy) + static_cast<long long>(j) * lights
+                          : lights * light_extra + cl + static_cast<long long>(j - light_extra) * ncl;
     } else {
-      t = lights * light_extra + cl + j * ncl;
+      t = lights * light_extra + cl + static_cast<long long>(j) * ncl;
     }
-    if (t >= plan1.items) return false;
+    if (t >= plan1.items) return;
     it.job = 1;
-    place(p1, plan1, J1::B_MN, t, it);
-    return true;
+    place(p1, plan1, J1::B_MN, static_cast<int>(t), it);
   };
+  PgWalk<decltype(item_at)> walk(item_at, lane);
+  PgItem it;
 
   if (warp == 0) {
-    // ------------------------------------------------------------------ TMA producer (both CTAs)
-    if (lane == 0) {
+    // ------------------------------------------------------------------ TMA producer (both CTAs; lane 0 issues)
+    {
       int s = 0, issued = 0;
       uint32_t ph = 0;
       bool ok = true;
       auto bytes_of = [&](const PgItem& it, const PairGemmParams& p, bool b_mn) {
-        return static_cast<uint32_t>(kPgTileBytes + (b_mn ? it.wide * 64 : p.bn * 64));
+        return static_cast<uint32_t>(kPgTileBytes + (b_mn && !p.b_blocks ? it.wide * 64 : p.bn * 64));
       };
-      auto load_a = [&](bool mn, const CUtensorMap& tm, int st, int kb, int m0) {
-        const uint32_t bar = dsmem_addr(&full[st], 0);
+      // One thread issues everything for a stage within the time of its MMAs (512 cycles at most), so addresses are kept
+      // as offsets from a few bases.
+      const uint32_t full0 = dsmem_addr(&full[0], 0), a0 = smem_u32(sA), b0 = smem_u32(sB);
+      auto load_a = [&](bool mn, const CUtensorMap* tm, int st, int k, int m0) {
+        const uint32_t bar = full0 + 8u * st, dst = a0 + static_cast<uint32_t>(st * kPgTileBytes);
         if (mn) {
-          tma_load_2d_pair(sA + st * kPgTileBytes, &tm, bar, m0, kb * kK);
-          tma_load_2d_pair(sA + st * kPgTileBytes + 8192, &tm, bar, m0 + 64, kb * kK);
+          tma_load_3d_pair_at(dst, tm, bar, 0, k, m0 >> 6);
         } else {
-          tma_load_2d_pair(sA + st * kPgTileBytes, &tm, bar, kb * kK, m0);
+          tma_load_2d_pair_at(dst, tm, bar, k, m0);
         }
       };
       // K-major: one box of bn / 2 rows, of which a narrower last tile uses the first ones
-      auto load_b = [&](bool mn, const CUtensorMap& tm, int st, int kb, int n0, int wide) {
-        const uint32_t bar = dsmem_addr(&full[st], 0);
-        if (mn) {
-          for (int j = 0; j < wide / 128; ++j)
-            tma_load_2d_pair(sB + st * kPgTileBytes + j * 8192, &tm, bar, n0 + 64 * j, kb * kK);
+      auto load_b = [&](bool mn, bool blocks, const CUtensorMap* tm, int st, int k, int n0, int wide) {
+        const uint32_t bar = full0 + 8u * st, dst = b0 + static_cast<uint32_t>(st * kPgTileBytes);
+        if (mn && blocks) {
+          tma_load_3d_pair_at(dst, tm, bar, 0, k, n0 >> 6);
+        } else if (mn) {
+          tma_load_2d_pair_at(dst, tm, bar, n0, k);
+          if (wide > 128) tma_load_2d_pair_at(dst + 8192, tm, bar, n0 + 64, k);
         } else {
-          tma_load_2d_pair(sB + st * kPgTileBytes, &tm, bar, kb * kK, n0);
+          tma_load_2d_pair_at(dst, tm, bar, k, n0);
         }
       };
-      PgItem it;
       int ahead = 0;  // stages whose B is already on its way
+      bool more = walk.next(it);
       if (!TWO && p0.early == PG_EARLY_B) {
-        if (item_at(0, it)) {
+        if (more) {
           ahead = min(kPgStages, it.kb1 - it.kb0);
-          for (int st = 0; st < ahead; ++st) {  // every stage is free at the start
-            if (leader) mbar_arrive_expect_tx(&full[st], 2 * bytes_of(it, p0, J0::B_MN));
-            load_b(J0::B_MN, tm_b0, st, it.kb0 + st, it.nt * p0.bn + static_cast<int>(rank) * (it.wide / 2), it.wide);
-          }
+          if (lane == 0)
+            for (int st = 0; st < ahead; ++st) {  // every stage is free at the start
+              if (leader) mbar_arrive_expect_tx(&full[st], 2 * bytes_of(it, p0, J0::B_MN));
+              load_b(J0::B_MN, p0.b_blocks, &tm_b0, st, (it.kb0 + st) * kK, it.nt * p0.bn + static_cast<int>(rank) * (it.wide / 2), it.wide);
+            }
         }
         grid_dep_wait();
       }
-      for (int i = 0; ok && item_at(i, it); ++i) {
+      for (; ok && more; more = walk.next(it)) {
         const bool second = TWO && it.job == 1;
         const PairGemmParams& p = second ? p1 : p0;
-        const CUtensorMap& tm_a = second ? tm_a1 : tm_a0;
-        const CUtensorMap& tm_b = second ? tm_b1 : tm_b0;
+        const CUtensorMap* tm_a = second ? &tm_a1 : &tm_a0;
+        const CUtensorMap* tm_b = second ? &tm_b1 : &tm_b0;
         const bool a_mn = second ? J1::A_MN : J0::A_MN, b_mn = second ? J1::B_MN : J0::B_MN;
-        const uint32_t stage_bytes = bytes_of(it, p, b_mn);
+        const uint32_t stage_bytes = 2 * bytes_of(it, p, b_mn);
         const int m0 = it.mt * 256 + static_cast<int>(rank) * 128;
         const int n0 = it.nt * p.bn + static_cast<int>(rank) * (it.wide / 2);
         for (int kb = it.kb0; kb < it.kb1; ++kb) {
-          if (issued >= ahead) {
-            if (!mbar_wait_cluster(&empty[s], ph ^ 1u, abort_flag)) {
-              ok = false;
-              break;
-            }
-            if (leader) mbar_arrive_expect_tx(&full[s], 2 * stage_bytes);
-            load_b(b_mn, tm_b, s, kb, n0, it.wide);
+          if (issued >= ahead && !__all_sync(0xffffffffu, mbar_wait_cluster(&empty[s], ph ^ 1u, abort_flag))) {
+            ok = false;
+            break;
           }
-          load_a(a_mn, tm_a, s, kb, m0);
+          if (lane == 0) {
+            if (issued >= ahead) {
+              if (leader) mbar_arrive_expect_tx(&full[s], stage_bytes);
+              load_b(b_mn, p.b_blocks, tm_b, s, kb * kK, n0, it.wide);
+            }
+            load_a(a_mn, tm_a, s, kb * kK, m0);
+          }
+          __syncwarp();
           ++issued;
           if (++s == kPgStages) {
             s = 0;
@@ -336,7 +375,7 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tm_a0, const C
         }
       }
       grid_dep_launch();  // all loads issued: the next kernel may be scheduled onto SMs as they free up
-      if (ok) {
+      if (ok && lane == 0) {
         // The release of the last use of every stage, so that no arrival on this CTA's barriers (an MMA commit
         // completes asynchronously) is still in flight when the CTA exits.
         for (int i = 0; i < kPgStages; ++i) {
@@ -347,7 +386,7 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tm_a0, const C
           }
         }
       }
-      if (!ok && leader) {
+      if (!ok && leader && lane == 0) {
         // Gave up: let the pair's copies still in flight land (bounded) before shared memory goes.
         const int pending = issued < kPgStages ? issued : kPgStages;
         for (int i = 1; i <= pending; ++i) {
@@ -365,59 +404,65 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tm_a0, const C
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ pair MMA issuer (leader)
-    if (lane == 0 && leader) {
+    if (leader) {  // lane 0 issues
       int s = 0;
       uint32_t ph = 0;
       int acc = 0;
       uint32_t acc_ph = 0;
       bool ok = true;
-      PgItem it;
-      for (int i = 0; ok && item_at(i, it); ++i) {
+      while (ok && walk.next(it)) {
         const bool second = TWO && it.job == 1;
         const int kchunk = second ? p1.kchunk : p0.kchunk;
         const bool a_mn = second ? J1::A_MN : J0::A_MN, b_mn = second ? J1::B_MN : J0::B_MN;
         const uint32_t idesc = KIND == PG_I8 ? make_idesc_i8(256, it.wide)
                                              : make_idesc_bf16(256, it.wide) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+        // Descriptors of stage 0; a stage on adds 16 KB, an MMA on 32 bytes of every row (K-major) or 16 lines (MN-major),
+        // all in units of 16 bytes.
+        const uint32_t a_addr = smem_u32(sA), b_addr = smem_u32(sB);
+        const uint64_t da0 = a_mn ? make_sdesc_mn_sw128(a_addr) : make_sdesc_sw128(a_addr);
+        const uint64_t db0 = b_mn ? make_sdesc_mn_sw128(b_addr) : make_sdesc_sw128(b_addr);
+        const uint64_t a_step = a_mn ? 128 : 2, b_step = b_mn ? 128 : 2;
         int kb = it.kb0;
         do {  // one accumulation; a tile without k still hands its (empty) accumulator on
           const int end = min(kb + kchunk, it.kb1);
-          if (!mbar_wait_cluster(&acc_empty[acc], acc_ph ^ 1u, abort_flag)) {
+          if (!__all_sync(0xffffffffu, mbar_wait_cluster(&acc_empty[acc], acc_ph ^ 1u, abort_flag))) {
             ok = false;
             break;
           }
           tc_fence_after_sync();
           const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 256);
           for (int first = kb; kb < end; ++kb) {
-            if (!mbar_wait_cluster(&full[s], ph, abort_flag)) {
+            if (!__all_sync(0xffffffffu, mbar_wait_cluster(&full[s], ph, abort_flag))) {
               ok = false;
               break;
             }
             tc_fence_after_sync();
-            const uint32_t a_addr = smem_u32(sA + s * kPgTileBytes);
-            const uint32_t b_addr = smem_u32(sB + s * kPgTileBytes);
+            uint64_t da = da0 + static_cast<uint64_t>(s * (kPgTileBytes / 16));
+            uint64_t db = db0 + static_cast<uint64_t>(s * (kPgTileBytes / 16));
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {  // K-major: 32 bytes of every row; MN-major: 16 lines
-              const uint64_t da = a_mn ? make_sdesc_mn_sw128(a_addr + k * 2048) : make_sdesc_sw128(a_addr + k * 32);
-              const uint64_t db = b_mn ? make_sdesc_mn_sw128(b_addr + k * 2048) : make_sdesc_sw128(b_addr + k * 32);
+            for (int k = 0; k < 4; ++k, da += a_step, db += b_step) {
               const uint32_t accumulate = (kb != first || k != 0) ? 1u : 0u;
+              if (lane != 0) continue;
               if (KIND == PG_I8)
                 tc_mma_i8_pair(d_tmem, da, db, idesc, accumulate);
               else
                 tc_mma_bf16_pair(d_tmem, da, db, idesc, accumulate);
             }
-            tc_commit_pair_mc(&empty[s], 0x3);  // frees stage s in both CTAs once read
+            if (lane == 0) tc_commit_pair_mc(&empty[s], 0x3);  // frees stage s in both CTAs once read
+            __syncwarp();
             if (++s == kPgStages) {
               s = 0;
               ph ^= 1u;
             }
           }
           if (!ok) break;
-          tc_commit_pair_mc(&acc_full[acc], 0x3);
+          if (lane == 0) tc_commit_pair_mc(&acc_full[acc], 0x3);
+          __syncwarp();
           acc ^= 1;
           if (acc == 0) acc_ph ^= 1u;
         } while (kb < it.kb1);
       }
-      if (!ok) {
+      if (!ok && lane == 0) {
         tc_commit_pair_mc(drain, 0x1);
         const unsigned long long t0 = globaltimer_ns();
         while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
@@ -431,7 +476,6 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tm_a0, const C
     const uint32_t leader_acc_empty1 = dsmem_addr(&acc_empty[1], 0);
     int acc = 0;
     uint32_t acc_ph = 0;
-    PgItem it;
     // One tile: false once a wait gave up.
     auto finish = [&](auto* job, const PairGemmParams& p, const auto& ep, const PgPlan& pl, int turn) {
       using Epi = typename std::remove_pointer_t<decltype(job)>::Epi;
@@ -439,8 +483,7 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tm_a0, const C
       tile.row0 = it.mt * 256 + static_cast<int>(rank) * 128 + q * 32;
       tile.n0 = it.nt * p.bn;
       tile.width = it.width;
-      tile.half = (warp - 2) >> 2;
-      tile.turn = turn;
+      tile.part = (((warp - 2) >> 2) + turn) % kParts;
       tile.nt = it.nt;
       tile.kz = it.kz;
       tile.M = pl.rows;
@@ -467,11 +510,11 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tm_a0, const C
       return true;
     };
     bool ok = true;
-    for (int i = 0; ok && item_at(i, it); ++i) {
+    for (int turn = 0; ok && walk.next(it); ++turn) {
       if (TWO && it.job == 1)
-        ok = finish(static_cast<J1*>(nullptr), p1, ep1, plan1, i);
+        ok = finish(static_cast<J1*>(nullptr), p1, ep1, plan1, turn);
       else
-        ok = finish(static_cast<J0*>(nullptr), p0, ep0, plan0, i);
+        ok = finish(static_cast<J0*>(nullptr), p0, ep0, plan0, turn);
     }
   }
 
@@ -484,7 +527,7 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tm_a0, const C
 }
 
 template <int KIND, class J>
-__global__ void __launch_bounds__(kPgThreads, 1)
+__global__ void __launch_bounds__(pair_gemm_threads(J::Epi::kParts), 1)
     k_pair_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                 const __grid_constant__ PairGemmParams p, const __grid_constant__ typename J::Params ep) {
   const PgNoEpi::Params none;
@@ -493,7 +536,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 
 // Two bf16 products in one launch.
 template <class J0, class J1>
-__global__ void __launch_bounds__(kPgThreads, 1)
+__global__ void __launch_bounds__(pair_gemm_threads(J0::Epi::kParts), 1)
     k_pair_gemm2(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_b0,
                  const __grid_constant__ PairGemmParams p0, const __grid_constant__ typename J0::Params ep0,
                  const __grid_constant__ CUtensorMap tm_a1, const __grid_constant__ CUtensorMap tm_b1,
