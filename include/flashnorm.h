@@ -321,9 +321,9 @@ FN_API fn_status flashnorm_nvfp4_workspace_bytes(int64_t M, int64_t d, int64_t N
  *   precedes; fold with g = 1), eps is then ignored.
  * flashnorm_glu_int8: Q and scales from the fold with glu = 1; y [M, F].
  * flashnorm_int8_workspace_bytes: the scratch a call of this shape needs on the current device, written to *bytes
- *   (codes, row scales, and for M <= FN_DECODE_MAX_M the partial sums of a split contraction). Caller-owned, 16-byte
- *   aligned, contents irrelevant before and after; calls whose kernels may overlap on the GPU must not share one. A
- *   smaller one returns FN_ERR_INVALID_ARG.
+ *   (codes and row scales; 0, and then NULL will do, for M <= FN_DECODE_MAX_M unless d is so large that the one-launch
+ *   kernel cannot keep the codes on chip). Caller-owned, 16-byte aligned, contents irrelevant before and after; calls
+ *   whose kernels may overlap on the GPU must not share one. A smaller one returns FN_ERR_INVALID_ARG.
  * Constraints: d % 16 == 0, 16 <= d <= 131072 (int32 sums), N % 8 == 0 (GLU: F % 16 == 0).
  */
 FN_API fn_status flashnorm_fold_weights_int8(const void* W, const void* g, void* Q, void* scales, int64_t d, int64_t N,

@@ -176,26 +176,37 @@ def _invoke(entry: str, lead: torch.Tensor, *args, report: str | None = None) ->
 
 # While prepare() records, on its own thread: the library calls made (size queries excepted) and every
 # tensor whose address was taken, which the prepared call keeps alive. Thread-local, so that calls made by
-# other threads meanwhile run as usual.
+# other threads meanwhile run as usual; _recorders, the number of threads that record, spares all calls the
+# thread-local lookups while none does.
 _rec = threading.local()
+_rec_lock = threading.Lock()
+_recorders = 0
 
 
 def _recording():
-    return getattr(_rec, "calls", None)
+    return getattr(_rec, "calls", None) if _recorders else None
+
+
+_entries = {}  # the library's functions by name
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _invoke_on(dev: int, entry: str, *args, report: str | None = None) -> None:
-    calls = _recording()
-    if calls is not None and not entry.endswith("_workspace_bytes"):
-        calls.append((dev, entry, args, report or entry))
-        return
-    lib = load_library()
-    if dev == torch.cuda.current_device():
-        status = getattr(lib, entry)(*args)
+    if _recorders:
+        calls = _recording()
+        if calls is not None and not entry.endswith("_workspace_bytes"):
+            calls.append((dev, entry, args, report or entry))
+            return
+    f = _entries.get(entry)
+    if f is None:
+        f = _entries[entry] = getattr(load_library(), entry)
+    if dev == _current_device():
+        status = f(*args)
     else:
         with torch.cuda.device(dev):
-            status = getattr(lib, entry)(*args)
-    _check(report or entry, status)
+            status = f(*args)
+    if status != FN_OK:
+        _check(report or entry, status)
 
 
 # The current stream's cudaStream_t as an integer; torch's internal accessor skips building a Stream object
@@ -213,9 +224,10 @@ def _ptr(t):
     """A tensor's device address for a void* argument (None passes NULL)."""
     if t is None:
         return None
-    keep = getattr(_rec, "keep", None)
-    if keep is not None:
-        keep.append(t)
+    if _recorders:
+        keep = getattr(_rec, "keep", None)
+        if keep is not None:
+            keep.append(t)
     return t.data_ptr()
 
 
@@ -249,11 +261,16 @@ def prepare(func, *args, **kwargs) -> PreparedCall:
     and any scratch the call chose (a workspace="auto" buffer is allocated here and kept)."""
     if _recording() is not None:
         raise RuntimeError("prepare() does not nest")
+    global _recorders
     rec, keep = [], []
     _rec.calls, _rec.keep = rec, keep
+    with _rec_lock:
+        _recorders += 1
     try:
         result = func(*args, **kwargs)
     finally:
+        with _rec_lock:
+            _recorders -= 1
         _rec.calls, _rec.keep = None, None
     if len(rec) != 1:
         raise ValueError(f"prepare() takes a call that makes one library call; this one made {len(rec)}")
@@ -287,7 +304,7 @@ def _out_code(out_dtype) -> int:
 
 def _output(out, shape, dtype, like):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     _need(out, "out", dtype)
     if tuple(out.shape) != tuple(shape):
         raise ValueError(f"out must have shape {tuple(shape)}, got {tuple(out.shape)}")
@@ -661,7 +678,7 @@ def flashnorm_rope(x: torch.Tensor, rope_cs: torch.Tensor, positions: torch.Tens
     if x.stride(2) != 1 and hd > 1:
         raise ValueError("the features of a head must be contiguous")
     if out is None:
-        out = torch.empty((M, H, hd), dtype=x.dtype, device=x.device)
+        out = x.new_empty((M, H, hd))
     elif out is not x:
         if not isinstance(out, torch.Tensor) or out.dtype != x.dtype:
             raise TypeError(f"out must be a {x.dtype} tensor")
@@ -748,7 +765,9 @@ def _call_workspace(workspace, nbytes: int, x: torch.Tensor):
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError('workspace must be "auto" or a uint8 CUDA tensor')
-        return torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        if nbytes == 0:
+            return None
+        return x.new_empty(nbytes, dtype=torch.uint8)
     _need(workspace, "workspace", torch.uint8, dim=1)
     _same_device(x, workspace=workspace)
     return workspace
@@ -779,7 +798,7 @@ def flashnorm_linear_int8(x: torch.Tensor, Q: torch.Tensor, scales: torch.Tensor
         return y
     ws = _call_workspace(workspace, flashnorm_int8_workspace_bytes(M, d, N, False, x.get_device()), x)
     _invoke("flashnorm_linear_int8", x, _ptr(x), _ptr(Q), _ptr(scales), _ptr(y), M, d, N, float(eps), int(bool(norm)),
-            _out_code(out_dtype), _ptr(ws), ws.numel(), _stream_ptr(x))
+            _out_code(out_dtype), _ptr(ws), ws.numel() if ws is not None else 0, _stream_ptr(x))
     return y
 
 
@@ -793,7 +812,7 @@ def flashnorm_glu_int8(x: torch.Tensor, Q_gu: torch.Tensor, scales: torch.Tensor
         return y
     ws = _call_workspace(workspace, flashnorm_int8_workspace_bytes(M, d, F, True, x.get_device()), x)
     _invoke("flashnorm_glu_int8", x, _ptr(x), _ptr(Q_gu), _ptr(scales), _ptr(y), M, d, F, float(eps),
-            _out_code(out_dtype), _ptr(ws), ws.numel(), _stream_ptr(x))
+            _out_code(out_dtype), _ptr(ws), ws.numel() if ws is not None else 0, _stream_ptr(x))
     return y
 
 
@@ -838,13 +857,13 @@ def flashnorm_linear_cross_entropy(x: torch.Tensor, Wstar: torch.Tensor, targets
     ignore_index has loss 0. workspace: "auto", or a uint8 CUDA tensor of at least
     flashnorm_cross_entropy_workspace_bytes(M, d, V) bytes."""
     M, d, V = _ce_call(x, Wstar, targets)
-    loss = torch.empty(M, dtype=torch.float32, device=x.device)
-    lse = torch.empty(M, dtype=torch.float32, device=x.device)
+    loss = x.new_empty(M, dtype=torch.float32)
+    lse = x.new_empty(M, dtype=torch.float32)
     if M == 0:
         return loss, lse
     ws = _call_workspace(workspace, flashnorm_cross_entropy_workspace_bytes(M, d, V, False, x.get_device()), x)
     _invoke("flashnorm_linear_cross_entropy", x, _ptr(x), _ptr(Wstar), _ptr(targets), _ptr(loss), _ptr(lse), M, d, V,
-            float(eps), int(ignore_index), _ptr(ws), ws.numel(), _stream_ptr(x))
+            float(eps), int(ignore_index), _ptr(ws), ws.numel() if ws is not None else 0, _stream_ptr(x))
     return loss, lse
 
 
@@ -864,7 +883,7 @@ def flashnorm_linear_cross_entropy_backward(grad_loss: torch.Tensor, x: torch.Te
     dW = torch.empty_like(Wstar)
     ws = _call_workspace(workspace, flashnorm_cross_entropy_workspace_bytes(M, d, V, True, x.get_device()), x)
     _invoke("flashnorm_linear_cross_entropy_backward", x, _ptr(grad_loss), _ptr(x), _ptr(Wstar), _ptr(targets),
-            _ptr(lse), _ptr(dx), _ptr(dW), M, d, V, float(eps), int(ignore_index), _ptr(ws), ws.numel(), _stream_ptr(x))
+            _ptr(lse), _ptr(dx), _ptr(dW), M, d, V, float(eps), int(ignore_index), _ptr(ws), ws.numel() if ws is not None else 0, _stream_ptr(x))
     return dx, dW
 
 

@@ -13,6 +13,35 @@ int int8_ksplit(int64_t n_rows, int64_t d, int sms) {
   return static_cast<int>(std::max<int64_t>(1, std::min(2 * sms / slabs, num_kb)));
 }
 
+// How the one-launch decode kernel runs a shape; ranks 0: it does not (the codes of a K range leave too little shared
+// memory for the ring, at large d with so many slabs that few ranks fit).
+struct Int8Cluster {
+  int slabs, ranks, max_kb, stages;
+};
+
+Int8Cluster int8_cluster_plan(int64_t M, int64_t d, int64_t n_rows, int sms) {
+  Int8Cluster c = {};
+  if (M > FN_DECODE_MAX_M) return c;
+  const int64_t num_kb = (d + 127) / 128;
+  const int64_t slabs = (n_rows + fn::kI8Rows - 1) / fn::kI8Rows;
+  // a power of two of ranks that fits two CTAs per SM: clusters of 3 leave SMs empty and run in two waves (N = 12288,
+  // d = 4096: 22 us with 3, 15 with 2, 20 with 1 or, in two waves, 4)
+  int64_t ranks = 1;
+  while (2 * ranks <= std::min<int64_t>({2 * sms / slabs, num_kb, fn::kI8cMaxRanks})) ranks *= 2;
+  const int64_t max_kb = (num_kb + ranks - 1) / ranks;
+  // two CTAs per SM where the grid needs them (1 KB of each CTA's share is the system's)
+  const int64_t budget = slabs * ranks <= sms ? 227 * 1024 : 228 * 1024 / 2 - 1024;
+  if (max_kb > 256) return c;
+  const int64_t rest = budget - fn::int8_cluster_smem_bytes(static_cast<int>(M), static_cast<int>(max_kb), 0);
+  const int64_t stages = std::min<int64_t>({rest / fn::kI8WStage, max_kb, 16});
+  if (stages < std::min<int64_t>(max_kb, 3)) return c;
+  c.slabs = static_cast<int>(slabs);
+  c.ranks = static_cast<int>(ranks);
+  c.max_kb = static_cast<int>(max_kb);
+  c.stages = static_cast<int>(stages);
+  return c;
+}
+
 // The workspace of one call: where its parts start, and its size.
 struct Int8Workspace {
   int64_t counters, rho, xq, part, bytes;
@@ -20,7 +49,8 @@ struct Int8Workspace {
 };
 
 Int8Workspace int8_workspace(int64_t M, int64_t d, int64_t n_rows, int sms) {
-  Int8Workspace w;
+  Int8Workspace w = {};
+  if (int8_cluster_plan(M, d, n_rows, sms).ranks) return w;
   const bool decode = M <= FN_DECODE_MAX_M;
   const int64_t slabs = (n_rows + fn::kI8Rows - 1) / fn::kI8Rows;
   w.ksplit = decode ? int8_ksplit(n_rows, d, sms) : 1;
@@ -65,6 +95,21 @@ fn_status launch_int8_decode(const CUtensorMap& tw, const CUtensorMap& tx, const
   return FN_OK;
 }
 
+template <bool GLU, bool OUT_F32>
+fn_status launch_int8_cluster(const CUtensorMap& tw, const fn::Int8ClusterParams& p, int slabs, int dev, cudaStream_t s) {
+  auto kern = fn::k_decode_int8_cluster<GLU, OUT_F32>;
+  static bool configured[kMaxDevices] = {false};
+  if (!configured[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute (int8 cluster decode)");
+    configured[dev] = true;
+  }
+  cudaError_t e = launch_kernel(kern, dim3(static_cast<unsigned>(slabs * p.ranks)), dim3(fn::kI8cThreads),
+                                fn::int8_cluster_smem_bytes(p.M, p.max_kb, p.stages), s, p.ranks, tw, p);
+  if (e != cudaSuccess) return cuda_fail(e, "int8 cluster decode launch");
+  return FN_OK;
+}
+
 fn_status run_int8(const void* x, const void* Q, const void* scales, void* y, int64_t M, int64_t d, int64_t N, float eps,
                    int norm, int out_dtype, bool glu, void* workspace, int64_t workspace_bytes, cudaStream_t s) {
   fn_status st = check_int8_shape(M, d, N, glu);
@@ -78,11 +123,34 @@ fn_status run_int8(const void* x, const void* Q, const void* scales, void* y, in
   if ((st = check_ptr(Q, "Q")) != FN_OK) return st;
   if ((st = check_ptr(scales, "scales")) != FN_OK) return st;
   if ((st = check_ptr(y, "y")) != FN_OK) return st;
-  if ((st = check_ptr(workspace, "workspace")) != FN_OK) return st;
+  if (M > FN_DECODE_MAX_M && (st = check_ptr(workspace, "workspace")) != FN_OK) return st;
   int dev = 0;
   const int sms = device_sm_count(&dev);
   if (sms <= 1) return fail(FN_ERR_CUDA, "cannot query the current device");
   const int64_t n_rows = glu ? 2 * N : N;
+  const Int8Cluster c = int8_cluster_plan(M, d, n_rows, sms);
+  if (c.ranks) {
+    CUtensorMap tw;
+    if ((st = make_u8_map(&tw, Q, d, n_rows, fn::kI8Rows)) != FN_OK) return st;
+    fn::Int8ClusterParams p;
+    p.x = static_cast<const uint16_t*>(x);
+    p.y = y;
+    p.scale = static_cast<const float*>(scales);
+    p.M = static_cast<int>(M);
+    p.K = static_cast<int>(d);
+    p.num_kb = static_cast<int>((d + 127) / 128);
+    p.n_rows = static_cast<int>(n_rows);
+    p.n_out = static_cast<int>(N);
+    p.ranks = c.ranks;
+    p.stages = c.stages;
+    p.max_kb = c.max_kb;
+    p.eps = eps;
+    p.norm = norm;
+    const bool f32 = out_dtype == FN_F32;
+    if (glu) return f32 ? launch_int8_cluster<true, true>(tw, p, c.slabs, dev, s) : launch_int8_cluster<true, false>(tw, p, c.slabs, dev, s);
+    return f32 ? launch_int8_cluster<false, true>(tw, p, c.slabs, dev, s) : launch_int8_cluster<false, false>(tw, p, c.slabs, dev, s);
+  }
+  if ((st = check_ptr(workspace, "workspace")) != FN_OK) return st;
   const Int8Workspace w = int8_workspace(M, d, n_rows, sms);
   if (workspace_bytes < w.bytes)
     return fail(FN_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes, (long long)w.bytes);

@@ -121,18 +121,14 @@ fn_status flashnorm_rope_table_scaled(void* rope_cs, int64_t max_pos, int64_t ro
   p.max_pos = static_cast<int>(max_pos);
   p.half = static_cast<int>(rot_dim / 2);
   p.kind = scaling;
-  p.base = base, p.factor = factor, p.original = original_max_pos, p.alpha = alpha, p.beta = beta;
+  const long double D = static_cast<long double>(rot_dim);
+  p.log2_base = static_cast<double>(std::log2(static_cast<long double>(base)) +
+                                    (scaling == FN_ROPE_SCALE_NTK ? std::log2(static_cast<long double>(factor)) * D / (D - 2) : 0.0L));
+  p.factor = factor, p.original = original_max_pos, p.alpha = alpha, p.beta = beta;
   p.mscale = attention_factor;
-  // positions per thread: up to kRopeTablePos once there are threads enough to fill the device, at least four
-  int dev = 0;
-  const int sms = device_sm_count(&dev);
-  if (sms <= 0) return fail(FN_ERR_CUDA, "cannot query the current device");
-  const int64_t per = std::min<int64_t>(fn::kRopeTablePos, std::max<int64_t>(4, max_pos * p.half / (int64_t{1024} * sms)));
-  p.pstep = (max_pos + per - 1) / per;
-  const int64_t blocks = (p.pstep * p.half + 255) / 256;
-  if (blocks > kMaxDim) return fail(FN_ERR_UNSUPPORTED, "table too large for one launch");
-  cudaError_t e = launch_kernel(fn::k_rope_table_scaled, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
-                                static_cast<cudaStream_t>(stream), 1, p);
+  const int64_t blocks = (max_pos + fn::kRopeTableBlock - 1) / fn::kRopeTableBlock;
+  cudaError_t e = launch_kernel(fn::k_rope_table_scaled, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>((p.half + 31) / 32)),
+                                dim3(256), 0, static_cast<cudaStream_t>(stream), 1, p);
   if (e != cudaSuccess) return cuda_fail(e, "scaled rope table launch");
   return FN_OK;
 }

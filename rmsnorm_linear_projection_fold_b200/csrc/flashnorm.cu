@@ -23,6 +23,7 @@
 #include "pair_gemm.cuh"
 #include "int8.cuh"
 #include "decode_int8.cuh"
+#include "decode_int8_cluster.cuh"
 #include "postnorm_pair.cuh"
 #include "postnorm_split.cuh"
 #include "rope.cuh"

@@ -81,24 +81,79 @@ __global__ void __launch_bounds__(256) k_fold_int8(const uint16_t* __restrict__ 
 
 // ---------------------------------------------------------------------------------------------- the row pass
 
-// Code of x in a row of largest magnitude a: 127 x / a to the nearest integer, ties to even, decided exactly. inv is
-// fp32 127 / a, so |x| inv is within 2^-16 of the true quotient; only a value that near to a tie needs a second look,
-// at 254 |x| against (2 k + 1) a, both exact in double.
-__device__ __forceinline__ uint32_t int8_code(float x, float a, float inv) {
-  const float p = x * inv;
-  float q = rintf(p);
-  if (fabsf(fabsf(p - q) - 0.5f) < 1.0f / 8192.0f) {
-    const float k = floorf(fabsf(p));
-    const double l = 254.0 * static_cast<double>(fabsf(x)), r = (2.0 * static_cast<double>(k) + 1.0) * static_cast<double>(a);
-    const bool up = l > r || (l == r && (static_cast<int>(k) & 1));
-    q = copysignf(up ? k + 1.0f : k, x);
+// Largest magnitude (two 16-bit ones: they order as unsigned bits, NaN above infinity) and sum of squares (two halves) so
+// far.
+__device__ __forceinline__ void int8_take(const uint4& v, uint64_t& ss, uint32_t& amax) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint64_t x = pack_f32x2(bf16lo_to_f32(w[e]), bf16hi_to_f32(w[e]));
+    ss = fma_f32x2(x, x, ss);
+    amax = __vmaxu2(amax, w[e] & 0x7FFF7FFFu);
   }
-  return static_cast<uint32_t>(static_cast<int>(q)) & 0xFFu;
 }
+
+// A row's scale, and the codes it gives: 127 x / a to the nearest integer, ties to even, decided exactly. A row with an
+// infinity or a NaN has zero codes and rho = NaN.
+struct Int8Row {
+  float a, inv, up, rho;
+  bool finite;
+  __device__ __forceinline__ Int8Row(uint32_t magnitude, float ss, int K, float eps, int norm) {
+    finite = magnitude < 0x7F80u;
+    a = __uint_as_float(magnitude << 16);
+    float r = __fdiv_rn(a, 127.0f);
+    if (norm) r *= 1.0f / sqrtf(ss / static_cast<float>(K) + eps);
+    rho = finite ? r : __int_as_float(0x7fc00000);
+    // rows near the ends of the exponent range are scaled by a power of two (exact), so that neither 127 / a nor 127 x
+    // overflows
+    up = a < 1e-30f ? 0x1p100f : a > 1e30f ? 0x1p-20f : 1.0f;
+    a *= up;
+    inv = finite && a > 0.f ? __fdiv_rn(127.0f, a) : 0.0f;
+  }
+  // Eight codes. x inv is within 2^-16 of the true quotient (inv is rounded once); adding 1.5 * 2^23 in the same fma rounds
+  // it to the nearest integer n, which the sum's low byte then holds. What is left of x inv shows how near to a tie it is;
+  // only there can n be wrong, and 127 x - n a decides: 127 x and n a have 16 bits, so the fma is exact.
+  __device__ __forceinline__ uint2 codes(const uint4& v) const {
+    if (!finite) return make_uint2(0u, 0u);
+    constexpr float kMagic = 12582912.0f;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const uint64_t ii = pack_f32x2(inv, inv), mm = pack_f32x2(kMagic, kMagic), neg = pack_f32x2(-1.0f, -1.0f);
+    uint64_t x[4];
+    uint32_t t[8];
+    float far = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = pack_f32x2(bf16lo_to_f32(w[e]), bf16hi_to_f32(w[e]));
+    if (up != 1.0f) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = mul_f32x2(x[e], pack_f32x2(up, up));
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint64_t r2 = fma_f32x2(x[e], ii, mm);
+      const float2 f = unpack_f32x2(fma_f32x2(x[e], ii, fma_f32x2(r2, neg, mm))), r = unpack_f32x2(r2);
+      far = fmaxf(far, fmaxf(fabsf(f.x), fabsf(f.y)));
+      t[2 * e] = __float_as_uint(r.x);
+      t[2 * e + 1] = __float_as_uint(r.y);
+    }
+    if (far > 0.5f - 1.0f / 8192.0f) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float2 xx = unpack_f32x2(x[e >> 1]);
+        const float n = __uint_as_float(t[e]) - kMagic, rest = fmaf(-n, a, 127.0f * (e & 1 ? xx.y : xx.x));
+        const float off = 2.0f * fabsf(rest);
+        if (off > a || (off == a && (t[e] & 1u))) t[e] = rest > 0.f ? t[e] + 1 : t[e] - 1;
+      }
+    }
+    uint2 o;
+    o.x = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
+    o.y = __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410);
+    return o;
+  }
+};
 
 // LPR threads per row, 256 / LPR rows per block; a thread keeps up to 4 x 8 elements of its row in registers, and a
 // longer row's remainder is read a second time (from L2). Also zeroes the `nzero` words at `zero`, the arrival
-// counters of a decode kernel that follows. A row with an infinity or a NaN gets zero codes and rho = NaN.
+// counters of a decode kernel that follows.
 // Bound: HBM, 2 bytes read and 1 written per element.
 template <int LPR>
 __global__ void __launch_bounds__(256) k_int8_rows(const uint16_t* __restrict__ x, int8_t* __restrict__ xq,
@@ -118,18 +173,9 @@ __global__ void __launch_bounds__(256) k_int8_rows(const uint16_t* __restrict__ 
   const uint4* src = reinterpret_cast<const uint4*>(x + static_cast<size_t>(live ? row : 0) * K);
   const int chunks = live ? K >> 3 : 0;
   uint4 held[kHeld];
-  float s0 = 0.f, s1 = 0.f;
-  uint32_t amax = 0;  // two 16-bit magnitudes
-  auto take = [&](const uint4& v) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float lo = bf16lo_to_f32(w[e]), hi = bf16hi_to_f32(w[e]);
-      s0 = fmaf(lo, lo, s0);
-      s1 = fmaf(hi, hi, s1);
-      amax = __vmaxu2(amax, w[e] & 0x7FFF7FFFu);  // magnitudes order as unsigned bits, NaN above infinity
-    }
-  };
+  uint64_t s2 = 0;
+  uint32_t amax = 0;
+  auto take = [&](const uint4& v) { int8_take(v, s2, amax); };
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) {
     const int c = sub + i * LPR;
@@ -139,7 +185,8 @@ __global__ void __launch_bounds__(256) k_int8_rows(const uint16_t* __restrict__ 
   for (int i = 0; i < kHeld; ++i) take(held[i]);
   for (int c = sub + kHeld * LPR; c < chunks; c += LPR) take(src[c]);
   uint32_t am = max(amax & 0xFFFFu, amax >> 16);
-  float ss = s0 + s1;
+  const float2 halves = unpack_f32x2(s2);
+  float ss = halves.x + halves.y;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     ss += __shfl_xor_sync(0xffffffffu, ss, o);
@@ -160,30 +207,10 @@ __global__ void __launch_bounds__(256) k_int8_rows(const uint16_t* __restrict__ 
     }
   }
   if (!live) return;
-  // tiny rows are scaled by 2^100 (exact) so that 127 / a does not overflow
-  float a = __uint_as_float(am << 16);
-  const bool finite = am < 0x7F80u;
-  const float up = a < 1e-30f ? 0x1p100f : 1.0f;
-  if (sub == 0) {
-    float r = __fdiv_rn(a, 127.0f);
-    if (norm) r *= 1.0f / sqrtf(ss / static_cast<float>(K) + eps);
-    rho[row] = finite ? r : __int_as_float(0x7fc00000);
-  }
-  a *= up;
-  const float inv = finite && a > 0.f ? __fdiv_rn(127.0f, a) : 0.0f;
+  const Int8Row q(am, ss, K, eps, norm);
+  if (sub == 0) rho[row] = q.rho;
   uint2* dst = reinterpret_cast<uint2*>(xq + static_cast<size_t>(row) * K);
-  auto put = [&](int c, const uint4& v) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t o[2] = {0u, 0u};
-    if (finite) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        o[e >> 1] |= int8_code(bf16lo_to_f32(w[e]) * up, a, inv) << (16 * (e & 1));
-        o[e >> 1] |= int8_code(bf16hi_to_f32(w[e]) * up, a, inv) << (16 * (e & 1) + 8);
-      }
-    }
-    dst[c] = make_uint2(o[0], o[1]);
-  };
+  auto put = [&](int c, const uint4& v) { dst[c] = q.codes(v); };
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) {
     const int c = sub + i * LPR;

@@ -27,47 +27,44 @@ struct RopeParams {
   float sign;     // +1, or -1 for the gradient
 };
 
-// One element of VEC consecutive features of type T, as floats.
+// VEC consecutive features of type T: 16 bytes as they lie in memory (or one feature).
 template <typename T, int VEC>
 struct RopeVec {
-  float f[VEC];
+  uint4 w;
   __device__ __forceinline__ void load(const T* p) {
-    if constexpr (VEC == 1) {
-      if constexpr (sizeof(T) == 2)
-        f[0] = __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(p)) << 16);
-      else
-        f[0] = *reinterpret_cast<const float*>(p);
-    } else {
-      const uint4 v = *reinterpret_cast<const uint4*>(p);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (sizeof(T) == 2) {
-          f[2 * e] = bf16lo_to_f32(w[e]);
-          f[2 * e + 1] = bf16hi_to_f32(w[e]);
-        } else {
-          f[e] = __uint_as_float(w[e]);
-        }
-      }
-    }
+    if constexpr (VEC == 1)
+      w.x = sizeof(T) == 2 ? *reinterpret_cast<const uint16_t*>(p) : *reinterpret_cast<const uint32_t*>(p);
+    else
+      w = *reinterpret_cast<const uint4*>(p);
   }
   __device__ __forceinline__ void store(T* p) const {
     if constexpr (VEC == 1) {
       if constexpr (sizeof(T) == 2)
-        *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(pack_bf16x2(f[0], 0.f) & 0xFFFFu);
+        *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w.x);
       else
-        *reinterpret_cast<float*>(p) = f[0];
+        *reinterpret_cast<uint32_t*>(p) = w.x;
     } else {
-      uint32_t w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (sizeof(T) == 2)
-          w[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
-        else
-          w[e] = __float_as_uint(f[e]);
-      }
-      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(p) = w;
     }
+  }
+  __device__ __forceinline__ void get(float (&f)[VEC]) const {
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+      f[e] = sizeof(T) == 4 ? __uint_as_float(v[e & 3]) : e & 1 ? bf16hi_to_f32(v[e >> 1]) : bf16lo_to_f32(v[e >> 1]);
+  }
+  __device__ __forceinline__ void set(const float (&f)[VEC]) {
+    uint32_t v[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      if constexpr (sizeof(T) == 4)
+        v[e] = __float_as_uint(f[e]);
+      else if (VEC == 1)
+        v[0] = pack_bf16x2(f[0], 0.f);
+      else if (e & 1)
+        v[e >> 1] = pack_bf16x2(f[e & ~1], f[e]);
+    }
+    w = make_uint4(v[0], v[1], v[2], v[3]);
   }
 };
 
@@ -77,7 +74,9 @@ struct RopeVec {
 // over); with VEC == 1 unit u < rot/2 is one pair and later units single features.
 //
 // Bound: HBM (each feature read and written once). A (cos, sin) pair is twice to four times as many bytes as the
-// feature it turns, so a thread keeps the pairs of its unit in registers and serves several heads with them.
+// feature it turns, so a thread keeps the pairs of its unit in registers and serves several heads with them. All heads of a
+// batch are loaded before any is stored (128 bytes in flight per thread): x and y may be the same memory, so the compiler
+// cannot reorder them itself.
 template <typename T, int VEC, bool HALF>
 __global__ void __launch_bounds__(256) k_rope(RopeParams p) {
   grid_dep_wait();
@@ -85,11 +84,12 @@ __global__ void __launch_bounds__(256) k_rope(RopeParams p) {
   const long long id = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
   if (id >= p.items) return;
   const int per_row = p.head_sets * p.units;
-  const long long m = id / per_row;
-  const int in_row = static_cast<int>(id - m * per_row);
-  const int hs = in_row / p.units, u = in_row - hs * p.units;
+  const long long m = p.items <= 0xffffffffll ? static_cast<uint32_t>(id) / static_cast<uint32_t>(per_row) : id / per_row;
+  const uint32_t in_row = static_cast<uint32_t>(id - m * per_row);
+  const int hs = static_cast<int>(in_row / static_cast<uint32_t>(p.units)), u = static_cast<int>(in_row) - hs * p.units;
   constexpr bool kPairUnits = HALF || VEC == 1;          // a rotated unit is VEC features and their partners
   constexpr int NP = kPairUnits ? VEC : VEC / 2;          // pairs of a unit
+  constexpr int kBatch = kPairUnits ? 4 : 8;              // heads in flight
   const int half = p.rot >> 1;
   const int rot_units = kPairUnits ? half / VEC : (p.rot + VEC - 1) / VEC;
   const bool turned = u < rot_units;
@@ -104,6 +104,21 @@ __global__ void __launch_bounds__(256) k_rope(RopeParams p) {
   } else {
     f0 = u * VEC;
   }
+  const T* x = static_cast<const T*>(p.x) + m * p.xs_row;
+  T* y = static_cast<T*>(p.y) + m * p.ys_row;
+  RopeVec<T, VEC> a[kBatch], b[kPairUnits ? kBatch : 1];
+  // heads that are only carried over stay where they are in place
+  auto has_work = [&](int h) { return h < p.H && !(p.in_place && !(turned && h < p.n_rope)); };
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = h0 + i * p.head_sets;
+      if (!has_work(h)) continue;
+      a[i].load(x + h * p.xs_head + f0);
+      if (kPairUnits && turned) b[kPairUnits ? i : 0].load(x + h * p.xs_head + f1);
+    }
+  };
+  load(hs);
   float c[NP], s[NP];
   if (turned && hs < p.n_rope) {
     const int pos = p.positions[m];
@@ -123,47 +138,50 @@ __global__ void __launch_bounds__(256) k_rope(RopeParams p) {
       atomicOr(&g_device_status, kStatusBadPosition);
     }
   }
-  const T* x = static_cast<const T*>(p.x) + m * p.xs_row;
-  T* y = static_cast<T*>(p.y) + m * p.ys_row;
-#pragma unroll 4
-  for (int h = hs; h < p.H; h += p.head_sets) {
-    const T* xh = x + h * p.xs_head;
-    T* yh = y + h * p.ys_head;
-    const bool rot = turned && h < p.n_rope;
-    if (!rot) {
-      if (p.in_place) continue;
-      RopeVec<T, VEC> a;
-      a.load(xh + f0);
-      a.store(yh + f0);
-      if (kPairUnits && turned) {
-        a.load(xh + f1);
-        a.store(yh + f1);
-      }
-      continue;
-    }
-    RopeVec<T, VEC> a;
-    a.load(xh + f0);
-    if constexpr (kPairUnits) {
-      RopeVec<T, VEC> b;
-      b.load(xh + f1);
+  for (int h0 = hs; h0 < p.H; h0 += kBatch * p.head_sets) {
+    if (h0 != hs) load(h0);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float t0 = a.f[j], t1 = b.f[j];
-        a.f[j] = t0 * c[j] - t1 * s[j];
-        b.f[j] = t0 * s[j] + t1 * c[j];
-      }
-      a.store(yh + f0);
-      b.store(yh + f1);
-    } else {
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = h0 + i * p.head_sets;
+      if (!has_work(h)) continue;
+      T* yh = y + h * p.ys_head;
+      if (turned && h < p.n_rope) {
+        float v[VEC];
+        a[i].get(v);
+        if constexpr (kPairUnits) {
+          float w[VEC];
+          b[i].get(w);
 #pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        const float t0 = a.f[2 * j], t1 = a.f[2 * j + 1];
-        if (f0 + 2 * j < p.rot) {
-          a.f[2 * j] = t0 * c[j] - t1 * s[j];
-          a.f[2 * j + 1] = t0 * s[j] + t1 * c[j];
+          for (int j = 0; j < VEC; ++j) {
+            const float t0 = v[j], t1 = w[j];
+            v[j] = t0 * c[j] - t1 * s[j];
+            w[j] = t0 * s[j] + t1 * c[j];
+          }
+          b[i].set(w);
+        } else {
+#pragma unroll
+          for (int j = 0; j < NP; ++j) {
+            const float t0 = v[2 * j], t1 = v[2 * j + 1];
+            if (f0 + 2 * j < p.rot) {
+              v[2 * j] = t0 * c[j] - t1 * s[j];
+              v[2 * j + 1] = t0 * s[j] + t1 * c[j];
+            }
+          }
+        }
+        // a pair past rot_dim keeps its bits: conversions there and back are exact, NaN payloads aside, so only whole
+        // units without such pairs go through them unconditionally
+        if constexpr (!kPairUnits && sizeof(T) == 2) {
+          const uint4 old = a[i].w;
+          a[i].set(v);
+          if (f0 + 2 >= p.rot) a[i].w.y = old.y;
+          if (f0 + 4 >= p.rot) a[i].w.z = old.z;
+          if (f0 + 6 >= p.rot) a[i].w.w = old.w;
+        } else {
+          a[i].set(v);
         }
       }
-      a.store(yh + f0);
+      a[i].store(yh + f0);
+      if (kPairUnits && turned) b[kPairUnits ? i : 0].store(yh + f1);
     }
   }
 }
@@ -178,45 +196,71 @@ __global__ void __launch_bounds__(256) k_rope(RopeParams p) {
 struct RopeTableParams {
   float* cs;
   int max_pos, half;
-  long long pstep;  // threads of one pair, and the distance between a thread's positions
   int kind;  // 0 none, 1 linear, 2 ntk, 3 yarn
-  double base, factor, original, alpha, beta, mscale;
+  double log2_base;  // ntk's factor included
+  double factor, original, alpha, beta, mscale;
 };
 
-constexpr int kRopeTablePos = 64;  // positions of one thread, at most
+// A block holds 32 pairs (one per lane) and kRopeTableBlock positions p0 + 32 k + j. An entry is the product of
+// exp(i theta j), in the registers of warp j % 8, and exp(i theta (p0 + 32 k)), in shared memory: two products and two
+// fused multiply-adds in double precision, whose error, a few 2^-53, is far under the fp32 rounding at the end. Each
+// thread starts from four sincospi and reaches the other factors by multiplication too. Angles are taken in half turns, so
+// that reducing a large one is exact. Bound: HBM writes; a sincos per entry, or even one per 55, is bound by the fp64
+// pipe's latency.
+constexpr int kRopeTableFine = 32, kRopeTableCoarse = 16, kRopeTableBlock = kRopeTableFine * kRopeTableCoarse;
 
-// A thread owns one pair and up to kRopeTablePos positions `pstep` apart. It takes the angle of its first position and
-// the step's angle in double precision, and reaches the others by complex multiplication in double precision (four
-// products each; 63 steps cost about 63 * 2^-52, far under the fp32 rounding at the end). Bound: HBM writes; one
-// fp64 sincos per entry instead is bound by the fp64 pipe.
+__device__ __forceinline__ double2 cmul(double2 a, double2 b) {
+  return make_double2(a.x * b.x - a.y * b.y, a.x * b.y + a.y * b.x);
+}
+__device__ __forceinline__ double2 turn_pi(double half_turns) {
+  double2 r;
+  sincospi(half_turns, &r.y, &r.x);
+  return r;
+}
+
 __global__ void __launch_bounds__(256) k_rope_table_scaled(RopeTableParams p) {
-  grid_dep_wait();
-  grid_dep_launch();
-  const long long id = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-  const int i = static_cast<int>(id % p.half);
-  const long long slot = id / p.half;  // threads of one pair: slots 0 .. pstep-1 start at position = slot
-  const long long pstep = p.pstep;
-  if (slot >= pstep) return;
-  const double D = 2.0 * p.half;
-  const double base = p.kind == 2 ? p.base * pow(p.factor, D / (D - 2.0)) : p.base;
-  double theta = pow(base, -2.0 * i / D);
+  __shared__ double2 coarse[kRopeTableCoarse][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int i = blockIdx.y * 32 + lane;
+  const long long p0 = static_cast<long long>(blockIdx.x) * kRopeTableBlock;
+  const int positions = static_cast<int>(min(static_cast<long long>(kRopeTableBlock), p.max_pos - p0));
+  double theta = exp2(-p.log2_base * (static_cast<double>(i) / p.half));
   if (p.kind == 1) theta /= p.factor;
   if (p.kind == 3) {
     const double turns = p.original * theta / 6.283185307179586476925;
     const double keep = fmin(fmax((turns - p.alpha) / (p.beta - p.alpha), 0.0), 1.0);
     theta *= keep + (1.0 - keep) / p.factor;
   }
-  double c, s, dc, ds;
-  sincos(static_cast<double>(slot) * theta, &s, &c);
-  sincos(static_cast<double>(pstep) * theta, &ds, &dc);
-  c *= p.mscale;
-  s *= p.mscale;
-  float2* out = reinterpret_cast<float2*>(p.cs) + i;
-  for (long long pos = slot; pos < p.max_pos; pos += pstep) {
-    out[pos * p.half] = make_float2(static_cast<float>(c), static_cast<float>(s));
-    const double nc = c * dc - s * ds;
-    s = c * ds + s * dc;
-    c = nc;
+  const double t = theta / 3.14159265358979323846;
+  double2 f[kRopeTableFine / 8];
+  {
+    const double2 step = turn_pi(8.0 * t), cstep = turn_pi(8.0 * kRopeTableFine * t);
+    f[0] = turn_pi(warp * t);
+    double2 c = turn_pi(static_cast<double>(p0 + kRopeTableFine * warp) * t);
+#pragma unroll
+    for (int k = 0; k < kRopeTableCoarse / 8; ++k) {
+      coarse[warp + 8 * k][lane] = c;
+      c = cmul(c, cstep);
+    }
+    f[0].x *= p.mscale;
+    f[0].y *= p.mscale;
+#pragma unroll
+    for (int j = 1; j < kRopeTableFine / 8; ++j) f[j] = cmul(f[j - 1], step);
+  }
+  __syncthreads();
+  grid_dep_wait();
+  grid_dep_launch();
+  if (i >= p.half) return;
+  float2* out = reinterpret_cast<float2*>(p.cs) + static_cast<size_t>(p0) * p.half + i;
+#pragma unroll 2
+  for (int k = 0; k * kRopeTableFine < positions; ++k) {
+    const double2 b = coarse[k][lane];
+#pragma unroll
+    for (int j = 0; j < kRopeTableFine / 8; ++j) {
+      const int pos = k * kRopeTableFine + warp + 8 * j;
+      const double2 v = cmul(f[j], b);
+      if (pos < positions) out[static_cast<size_t>(pos) * p.half] = make_float2(static_cast<float>(v.x), static_cast<float>(v.y));
+    }
   }
 }
 

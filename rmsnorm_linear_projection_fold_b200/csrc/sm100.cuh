@@ -199,9 +199,11 @@ __device__ __forceinline__ void dsmem_st_f32(uint32_t addr, float a) {
 // Every thread of every CTA in the cluster arrives; writes before it (including to other CTAs'
 // shared memory) are visible to all threads after it. Not the .aligned form: the lanes of a warp may
 // reach it at different times.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 
 // ---------------------------------------------------------------------------------------------

@@ -384,7 +384,7 @@ def test_int8_validation(lib):
     assert lin(P, P, P, P, 4, 576, 960, 1e-6, 1, 5, P, big, NULL) == fn.FN_ERR_INVALID_ARG       # out dtype
     assert lin(P, NULL, P, P, 4, 576, 960, 1e-6, 1, 0, P, big, NULL) == fn.FN_ERR_INVALID_ARG
     assert lin(P, P, P_MISALIGNED, P, 4, 576, 960, 1e-6, 1, 0, P, big, NULL) == fn.FN_ERR_ALIGN
-    assert lin(P, P, P, P, 4, 576, 960, 1e-6, 1, 0, NULL, 0, NULL) == fn.FN_ERR_INVALID_ARG      # no workspace
+    assert lin(P, P, P, P, 40, 576, 960, 1e-6, 1, 0, NULL, 0, NULL) == fn.FN_ERR_INVALID_ARG     # no workspace
     assert lin(P, P, P, P, 4, 576, 960, 1e-6, 1, 0, P, -1, NULL) == fn.FN_ERR_INVALID_ARG
     assert lin(P, P, P, P, 0, 576, 960, 1e-6, 1, 0, NULL, 0, NULL) == fn.FN_OK                   # empty call
     assert glu(P, P, P, P, 4, 576, 24, 1e-6, 0, P, big, NULL) == fn.FN_ERR_INVALID_ARG           # F % 16
