@@ -54,7 +54,7 @@ struct CePlan {
   int64_t pieces;
   int n_tiles;     // column tiles of a full piece
   int ksplit;      // K ranges of dx's product
-  int64_t rstd, part, tlogit;                        // forward
+  int64_t arrived, rstd, part, tlogit;               // forward
   int64_t n_live, rows, rank_of, target, u, hits, xc, P, acc, bytes;  // backward (and part)
 };
 
@@ -75,6 +75,8 @@ int ce_dx_ksplit(const fn::PairGemmParams& dx, const fn::PairGemmParams& dw, int
   return k;
 }
 
+// Up to so many rows the loss streams W* past the tokens (cross_entropy_small.cuh).
+constexpr int kCeSmallRows = 64;
 constexpr int kCeFwdParts = fn::CeFwdEpi<false>::kParts;
 
 constexpr int64_t kCePieceBytes = int64_t{64} << 20;  // of P, per piece
@@ -92,8 +94,14 @@ CePlan ce_plan(int64_t M, int64_t d, int64_t V, bool backward, int sms) {
   plan_pair_gemm(&g, M, c.piece, (d + 63) / 64, sms, 32);
   c.n_tiles = g.num_n_tiles;
   if (!backward) {
-    c.rstd = 0;
-    c.part = round_up(4 * M, 256);
+    c.arrived = 0;
+    c.rstd = 256;
+    c.part = c.rstd + round_up(4 * M, 256);
+    if (M <= kCeSmallRows) {
+      c.tlogit = c.part + round_up(8ll * sms * M, 256);
+      c.bytes = c.tlogit + round_up(4 * M, 256);
+      return c;
+    }
     c.tlogit = c.part + round_up(8ll * kCeFwdParts * c.n_tiles * M, 256);
     c.bytes = c.tlogit + round_up(4 * M, 256);
     return c;
@@ -143,6 +151,22 @@ fn_status launch_rstd(const void* x, float* rstd, int64_t M, int64_t d, float ep
   return e == cudaSuccess ? FN_OK : cuda_fail(e, "row statistics launch");
 }
 
+template <int NT>
+fn_status launch_ce_small(const CUtensorMap& tw, const CUtensorMap& tx, const fn::CeSmallParams& p, int sms, int dev,
+                          cudaStream_t s) {
+  auto kern = fn::k_ce_small<NT>;
+  constexpr int smem = fn::ce_small_smem_bytes(2 * NT);
+  static bool configured[kMaxDevices] = {false};
+  if (!configured[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute (cross entropy, few rows)");
+    configured[dev] = true;
+  }
+  const int slabs = (p.V + fn::kCsRows - 1) / fn::kCsRows;
+  cudaError_t e = launch_kernel(kern, dim3(static_cast<unsigned>(std::min(slabs, sms))), dim3(fn::kCsThreads), smem, s, 1, tw, tx, p);
+  return e == cudaSuccess ? FN_OK : cuda_fail(e, "cross entropy launch (few rows)");
+}
+
 }  // namespace
 
 extern "C" {
@@ -177,6 +201,31 @@ fn_status flashnorm_linear_cross_entropy(const void* x, const void* Wstar, const
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(workspace);
   float* rstd = reinterpret_cast<float*>(base + c.rstd);
+  if (M <= kCeSmallRows) {
+    fn::CeSmallParams p;
+    p.rstd = rstd;
+    p.tlogit = reinterpret_cast<float*>(base + c.tlogit);
+    p.targets = static_cast<const long long*>(targets);
+    p.part = reinterpret_cast<float2*>(base + c.part);
+    p.arrived = reinterpret_cast<unsigned*>(base + c.arrived);
+    p.loss = static_cast<float*>(loss);
+    p.lse = static_cast<float*>(lse);
+    p.M = static_cast<int>(M);
+    p.V = static_cast<int>(V);
+    p.num_kb = static_cast<int>((d + 63) / 64);
+    p.ignore = ignore_index;
+    const int tokens = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+    CUtensorMap tx, tw;
+    if ((st = make_k_map(&tx, x, d, M, d, tokens)) != FN_OK) return st;
+    if ((st = make_k_map(&tw, Wstar, d, V, d, fn::kCsRows)) != FN_OK) return st;
+    cudaError_t e = launch_kernel(fn::k_ce_rows_small, dim3(static_cast<unsigned>((M + 7) / 8)), dim3(256), 0, s, 1,
+                                  static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(Wstar), p.targets, rstd,
+                                  reinterpret_cast<float*>(base + c.tlogit), p.arrived, p.M, static_cast<int>(d), p.V, eps,
+                                  static_cast<long long>(ignore_index));
+    if (e != cudaSuccess) return cuda_fail(e, "cross entropy row pass launch");
+    return tokens == 16 ? launch_ce_small<8>(tw, tx, p, sms, dev, s)
+                        : tokens == 32 ? launch_ce_small<16>(tw, tx, p, sms, dev, s) : launch_ce_small<32>(tw, tx, p, sms, dev, s);
+  }
   fn::CeFwdParams ep;
   ep.rstd = rstd;
   ep.targets = static_cast<const long long*>(targets);

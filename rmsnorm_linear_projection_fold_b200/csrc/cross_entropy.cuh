@@ -173,15 +173,16 @@ struct CeFwdEpi {
   }
 };
 
-// lse and loss, one warp per row: each lane joins every 32nd partial pair, then the lanes join in a butterfly (a fixed
-// order). An ignored row's loss is 0; a target that is neither a class nor ignore_index gives NaN and is reported.
-__global__ void __launch_bounds__(256) k_ce_join(const float2* __restrict__ part, const float* __restrict__ tlogit,
-                                                 const long long* __restrict__ targets, float* __restrict__ loss,
-                                                 float* __restrict__ lse, int M, int V, int parts, long long ignore) {
-  grid_dep_wait();
-  grid_dep_launch();
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row >= M) return;
+// lse and loss of a row by LANES consecutive lanes: each joins every LANES-th partial pair, then they join in a butterfly (a
+// fixed order). An ignored row's loss is 0; a target that is neither a class nor ignore_index gives NaN and is reported.
+// Every lane of the warp calls, live or not.
+template <int LANES>
+__device__ __forceinline__ void ce_join_row(const float2* part, int parts, const float* tlogit, const long long* targets,
+                                            float* loss, float* lse, int row, bool live, int V, long long ignore, int lane) {
+  const int sub = lane % LANES;
+  const long long t = live ? targets[row] : ignore;
+  const float lt = live ? __ldcg(tlogit + row) : 0.f;  // not written, nor used, where t is no class
+  const float2* src = part + static_cast<size_t>(live ? row : 0) * parts;
   float m = -INFINITY, s = 0.f;
   auto join = [&](float qm, float qs) {
     const float mn = fmaxf(m, qm);
@@ -189,27 +190,44 @@ __global__ void __launch_bounds__(256) k_ce_join(const float2* __restrict__ part
     s = s * ex2(m - base) + qs * ex2(qm - base);
     m = mn;
   };
-  const float2* src = part + static_cast<size_t>(row) * parts;
-#pragma unroll 4
-  for (int i = lane; i < parts; i += 32) {
-    const float2 q = __ldcg(src + i);
-    join(q.x, q.y);
+  for (int i0 = sub; i0 < parts; i0 += 10 * LANES) {
+    float2 q[10];
+#pragma unroll
+    for (int k = 0; k < 10; ++k)
+      q[k] = live && i0 + k * LANES < parts ? __ldcg(src + i0 + k * LANES) : make_float2(-INFINITY, 0.f);
+    // the batch's maximum first: one exponential a pair instead of two
+    float mn = m;
+#pragma unroll
+    for (int k = 0; k < 10; ++k) mn = fmaxf(mn, q[k].x);
+    const float base = mn == -INFINITY ? 0.f : mn;
+    s *= ex2(m - base);
+#pragma unroll
+    for (int k = 0; k < 10; ++k) s = fmaf(q[k].y, ex2(q[k].x - base), s);
+    m = mn;
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) join(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
-  if (lane == 0) {
+  for (int o = LANES / 2; o > 0; o >>= 1) join(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
+  if (sub == 0 && live) {
     const float z = m * kLn2 + logf(s);
-    const long long t = targets[row];
     lse[row] = z;
     if (t == ignore) {
       loss[row] = 0.f;
     } else if (target_is_class(t, V)) {
-      loss[row] = z - __ldcg(tlogit + row);
+      loss[row] = z - lt;
     } else {
       loss[row] = __int_as_float(0x7fc00000);
       atomicOr(&g_device_status, kStatusBadTarget);
     }
   }
+}
+
+__global__ void __launch_bounds__(256) k_ce_join(const float2* __restrict__ part, const float* __restrict__ tlogit,
+                                                 const long long* __restrict__ targets, float* __restrict__ loss,
+                                                 float* __restrict__ lse, int M, int V, int parts, long long ignore) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  ce_join_row<32>(part, parts, tlogit, targets, loss, lse, row, row < M, V, ignore, lane);
 }
 
 // ---------------------------------------------------------------------------------------------- backward

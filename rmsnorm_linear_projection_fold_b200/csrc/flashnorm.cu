@@ -28,6 +28,7 @@
 #include "postnorm_split.cuh"
 #include "rope.cuh"
 #include "cross_entropy.cuh"
+#include "cross_entropy_small.cuh"
 
 namespace {
 
