@@ -53,9 +53,10 @@ struct CePlan {
   int64_t piece;   // vocabulary columns of a piece (forward: all)
   int64_t pieces;
   int n_tiles;     // column tiles of a full piece
-  int ksplit;      // K ranges of dx's product
+  int ksplit;      // K ranges of dx's product, and of dW*'s where it goes through planes
+  int dw_ksplit;
   int64_t arrived, rstd, part, tlogit;               // forward
-  int64_t n_live, rows, rank_of, target, u, hits, xc, P, acc, bytes;  // backward (and part)
+  int64_t n_live, rows, rank_of, target, u, hits, xc, P, acc, dw_acc, bytes;  // backward (and part)
 };
 
 // Stages per accumulation of the forward's logits: 1024 k keep the drift of the tensor core's sums near 1e-6.
@@ -64,14 +65,18 @@ constexpr int kCeFwdChunk = 16;
 // Tile width of the products whose B is MN-major (x or W*, [k][d]).
 int ce_mn_width(int64_t d) { return d > 128 ? 256 : 128; }
 
-// K ranges of dx's product: few enough planes, many enough items that its share of a pair's work fits into an even part
-// of both products'.
-int ce_dx_ksplit(const fn::PairGemmParams& dx, const fn::PairGemmParams& dw, int pairs) {
-  const int64_t items = static_cast<int64_t>(dx.num_m_tiles) * dx.num_n_tiles;
-  const int64_t all = items * dx.num_kb + static_cast<int64_t>(dw.num_m_tiles) * dw.num_n_tiles * dw.num_kb;
+// Up to so many classes, and with a row for every fourth at least, dW* is finished by a pass of its own (k_ce_dw), its
+// product cut into K ranges. With few rows the pass costs more than it saves (5 x 1080 x 1843: 9 us).
+constexpr int64_t kCeSmallVocab = 2048;
+
+// K ranges of a product that shares a launch with another: few enough planes, many enough items that the longest share of
+// any pair fits into an even part of both products' work.
+int ce_ksplit(const fn::PairGemmParams& g, const fn::PairGemmParams& other, int pairs) {
+  const int64_t items = static_cast<int64_t>(g.num_m_tiles) * g.num_n_tiles;
+  const int64_t all = items * g.num_kb + static_cast<int64_t>(other.num_m_tiles) * other.num_n_tiles * other.num_kb;
   const int64_t even = (all + pairs - 1) / pairs;
   int k = 1;
-  while (k < 64 && dx.num_kb / (k + 1) >= 8 && (items * k + pairs - 1) / pairs * ((dx.num_kb + k - 1) / k) > even) ++k;
+  while (k < 64 && g.num_kb / (k + 1) >= 8 && (items * k + pairs - 1) / pairs * ((g.num_kb + k - 1) / k) > even) ++k;
   return k;
 }
 
@@ -109,7 +114,8 @@ CePlan ce_plan(int64_t M, int64_t d, int64_t V, bool backward, int sms) {
   fn::PairGemmParams w;
   plan_pair_gemm_bn(&g, M, d, (c.piece + 63) / 64, ce_mn_width(d), 1);
   plan_pair_gemm_bn(&w, c.piece, d, (M + 63) / 64, ce_mn_width(d), 1);
-  c.ksplit = ce_dx_ksplit(g, w, sms / 2);
+  c.ksplit = ce_ksplit(g, w, sms / 2);
+  c.dw_ksplit = V <= kCeSmallVocab && 4 * M >= V ? ce_ksplit(w, g, sms / 2) : 0;
   const int64_t Mp = round_up(M, 64);  // the packed rows, zeros at their end
   c.n_live = 0;
   c.rows = 256;
@@ -121,7 +127,8 @@ CePlan ce_plan(int64_t M, int64_t d, int64_t V, bool backward, int sms) {
   c.xc = c.part + round_up(4ll * fn::CeGradEpi::kParts * c.n_tiles * c.pieces * M, 256);
   c.P = c.xc + round_up(2 * Mp * d, 256);
   c.acc = c.P + 2 * Mp * round_up(c.piece, 64);
-  c.bytes = c.acc + 4 * c.ksplit * M * d;
+  c.dw_acc = c.acc + round_up(4 * c.ksplit * M * d, 256);
+  c.bytes = c.dw_acc + 4 * c.dw_ksplit * c.piece * d;
   return c;
 }
 
@@ -318,17 +325,33 @@ fn_status flashnorm_linear_cross_entropy_backward(const void* g, const void* x, 
     plan_pair_gemm_bn(&q, width, d, (M + 63) / 64, ce_mn_width(d), 1);
     q.live = n_live;
     q.live_is_k = 1;
-    q.extra = std::max(1, p.num_kb / p.ksplit / q.num_kb);
-    const fn::CeDwParams we = {live, xc, static_cast<uint16_t*>(dWstar) + v0 * d, static_cast<int>(d), static_cast<int>(v0)};
     if ((st = make_mn_block_map(&ta1, P, ldp, Mp, ldp, 2)) != FN_OK) return st;
     if ((st = make_mn_operand(&tb1, &q, xc, d, Mp)) != FN_OK) return st;
-    st = launch_pair_gemm2<fn::PgJob<false, true, fn::CeDxEpi>, fn::PgJob<true, true, fn::CeDwEpi>>(
-        ta, tb, p, xe, ta1, tb1, q, we, sms, dev, s, "cross entropy gradients");
-    if (st != FN_OK) return st;
+    uint16_t* dWp = static_cast<uint16_t*>(dWstar) + v0 * d;
+    const char* what = "cross entropy gradients";
+    using Dx = fn::PgJob<false, true, fn::CeDxEpi>;
+    if (c.dw_ksplit) {
+      q.ksplit = c.dw_ksplit;
+      q.extra = std::max(1, p.num_kb / p.ksplit / std::max(1, q.num_kb / q.ksplit));
+      float* planes = reinterpret_cast<float*>(base + c.dw_acc);
+      const fn::CeDxParams we = {planes, static_cast<int>(d), 0};
+      st = launch_pair_gemm2<Dx, fn::PgJob<true, true, fn::CeDxEpi>>(ta, tb, p, xe, ta1, tb1, q, we, sms, dev, s, what);
+      if (st != FN_OK) return st;
+      e = launch_kernel(fn::k_ce_dw, dim3(static_cast<unsigned>(width)), dim3(256), 0, s, 1, static_cast<const float*>(planes), live,
+                        static_cast<const uint16_t*>(xc), dWp, static_cast<int>(width), static_cast<int>(d), c.dw_ksplit,
+                        static_cast<int>(v0));
+      if (e != cudaSuccess) return cuda_fail(e, "cross entropy dW launch");
+    } else {
+      q.extra = std::max(1, p.num_kb / p.ksplit / q.num_kb);
+      const fn::CeDwParams we = {live, xc, dWp, static_cast<int>(d), static_cast<int>(v0)};
+      st = launch_pair_gemm2<Dx, fn::PgJob<true, true, fn::CeDwEpi>>(ta, tb, p, xe, ta1, tb1, q, we, sms, dev, s, what);
+      if (st != FN_OK) return st;
+    }
   }
-  e = launch_kernel(fn::k_ce_dx, dim3(static_cast<unsigned>(M)), dim3(256), 0, s, 1, static_cast<const float*>(acc),
-                    static_cast<const float*>(cpart), static_cast<const fn::CeRow*>(rows), static_cast<const float*>(live.u),
-                    static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(Wstar),
+  const bool narrow = d <= 1024;  // a warp per row, else a block
+  e = launch_kernel(narrow ? fn::k_ce_dx<32> : fn::k_ce_dx<256>, dim3(static_cast<unsigned>(narrow ? (M + 7) / 8 : M)), dim3(256), 0, s,
+                    1, static_cast<const float*>(acc), static_cast<const float*>(cpart), static_cast<const fn::CeRow*>(rows),
+                    static_cast<const float*>(live.u), static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(Wstar),
                     static_cast<const int*>(rank_of), static_cast<uint16_t*>(dx), static_cast<int>(M), static_cast<int>(d),
                     c.ksplit, parts);
   return e == cudaSuccess ? FN_OK : cuda_fail(e, "cross entropy dx launch");

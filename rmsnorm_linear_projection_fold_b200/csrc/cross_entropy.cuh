@@ -584,7 +584,8 @@ struct CeDwEpi {
   }
 };
 
-// dx: fp32 sums over the pieces of the vocabulary, one plane per K range; the first piece writes, later ones add.
+// fp32 sums, one plane per K range: dx's over the pieces of the vocabulary (the first piece writes, later ones add), and
+// dW*'s where the vocabulary is small (k_ce_dw).
 struct CeDxParams {
   float* acc;  // [K ranges][M][ld]
   int ld;      // a multiple of 8
@@ -601,6 +602,10 @@ struct CeDxEpi {
       tmem_ld16(t.t_row + ch * 16, v);
       tmem_ld_wait();
       reg_fence16(v);
+      if (t.empty) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = 0u;
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) pg_put(t.stage, lane, j, make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
       __syncwarp();
@@ -623,8 +628,94 @@ struct CeDxEpi {
   }
 };
 
-// dx[m, :] = sum of the planes + u[m] W*[t, :] - x[m, :] (r^2 / d) c[m], one block per row; planes and partial sums c by the row's rank among
-// the live ones, in a fixed order.
+// dW*[n, :] = sum of the planes + sum over the live rows m with t[m] = n of u[m] x[m, :], one block per class. Used where
+// the vocabulary is small: 32 classes then have so many rows that one warp's list of them would take longer than the
+// tile's MMAs (the epilogue's way took 147 us at 2167 x 280 x 602, and 268 at 4096 x 64 x 128, where the one tile of dW*
+// had to run through all rows besides), and planes are cheap. The block looks through 2048 targets at a time, lists its
+// own in order, and its threads share out columns (8 each) and, where there are fewer column groups than threads, rows.
+__global__ void __launch_bounds__(256) k_ce_dw(const float* __restrict__ acc, const CeLive live, const uint16_t* __restrict__ xc,
+                                               uint16_t* __restrict__ dW, int N, int K, int planes, int v0) {
+  __shared__ int list[2048];
+  __shared__ int counts[8];
+  __shared__ float part[256 * 8];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int n = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rows = __ldcg(live.n_live), chunks = K >> 3;
+  const int width = min(chunks, 256), groups = 256 / width;  // column groups side by side, shares of the rows
+  const int col = threadIdx.x % width, share = threadIdx.x / width;
+  for (int c0 = 0; c0 < chunks; c0 += width) {
+    const int c = c0 + col;
+    float a[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a[e] = 0.f;
+    for (int r0 = 0; r0 < rows; r0 += 2048) {
+      int t[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = r0 + 256 * warp + 32 * i + lane;
+        t[i] = r < rows ? __ldcg(live.target + r) : -1;
+      }
+      unsigned hit[8];
+      int mine = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        hit[i] = __ballot_sync(0xffffffffu, t[i] == v0 + n);
+        mine += __popc(hit[i]);
+      }
+      if (lane == 0) counts[warp] = mine;
+      __syncthreads();
+      int at = 0, total = 0;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        if (w < warp) at += counts[w];
+        total += counts[w];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (hit[i] >> lane & 1u) list[at + __popc(hit[i] & ((1u << lane) - 1u))] = r0 + 256 * warp + 32 * i + lane;
+        at += __popc(hit[i]);
+      }
+      __syncthreads();
+      if (share < groups && c < chunks) {
+#pragma unroll 4
+        for (int k = share; k < total; k += groups) {
+          const int r = list[k];
+          const float u = __ldcg(live.u + r);
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(xc + static_cast<size_t>(r) * K) + c);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            a[2 * e] = fmaf(u, bf16lo_to_f32(w[e]), a[2 * e]);
+            a[2 * e + 1] = fmaf(u, bf16hi_to_f32(w[e]), a[2 * e + 1]);
+          }
+        }
+      }
+    }
+    if (groups > 1) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) part[threadIdx.x * 8 + e] = a[e];
+      __syncthreads();
+    }
+    if (share == 0 && c < chunks) {
+      for (int g = 1; g < groups; ++g)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] += part[(g * width + col) * 8 + e];
+      for (int z = 0; z < planes; ++z) {
+        const float4* src = reinterpret_cast<const float4*>(acc + (static_cast<size_t>(z) * N + n) * K) + 2 * c;
+        const float4 p = __ldcg(src), q = __ldcg(src + 1);
+        a[0] += p.x, a[1] += p.y, a[2] += p.z, a[3] += p.w, a[4] += q.x, a[5] += q.y, a[6] += q.z, a[7] += q.w;
+      }
+      reinterpret_cast<uint4*>(dW + static_cast<size_t>(n) * K)[c] =
+          make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7]));
+    }
+    __syncthreads();  // list, counts and part are used again
+  }
+}
+
+// dx[m, :] = sum of the planes + u[m] W*[t, :] - x[m, :] (r^2 / d) c[m], LPR threads per row; planes and partial sums c by
+// the row's rank among the live ones, in a fixed order. A thread's first 8 columns are on their way while c is summed.
+template <int LPR>
 __global__ void __launch_bounds__(256) k_ce_dx(const float* __restrict__ acc, const float* __restrict__ cpart,
                                                const CeRow* __restrict__ rows, const float* __restrict__ u,
                                                const uint16_t* __restrict__ x, const uint16_t* __restrict__ W,
@@ -633,35 +724,47 @@ __global__ void __launch_bounds__(256) k_ce_dx(const float* __restrict__ acc, co
   __shared__ float red[8];
   grid_dep_wait();
   grid_dep_launch();
-  const int row = blockIdx.x;
-  const int rank = __ldcg(rank_of + row);
+  const int row = blockIdx.x * (256 / LPR) + threadIdx.x / LPR, sub = threadIdx.x % LPR;
+  if (row >= M) return;  // whole warps; with a block per row there is no such block
+  const int rank = __ldcg(rank_of + row), chunks = K >> 3;
   uint4* dst = reinterpret_cast<uint4*>(dx + static_cast<size_t>(row) * K);
   if (rank < 0) {
     const bool bad = rank == kCeBad;
     const uint32_t w = bad ? 0x7FC07FC0u : 0u;
-    for (int c = threadIdx.x; c < (K >> 3); c += 256) dst[c] = make_uint4(w, w, w, w);
-    if (bad && threadIdx.x == 0) atomicOr(&g_device_status, kStatusBadTarget);
+    for (int c = sub; c < chunks; c += LPR) dst[c] = make_uint4(w, w, w, w);
+    if (bad && sub == 0) atomicOr(&g_device_status, kStatusBadTarget);
     return;
   }
-  float c = 0.f;
-  for (int i = threadIdx.x; i < parts; i += 256) c += __ldcg(cpart + static_cast<size_t>(i) * M + rank);
-  c = warp_sum(c);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = c;
-  __syncthreads();
-  c = ((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7]));
-  const float r = __ldcg(&rows[rank].rstd), ut = __ldcg(u + rank);
-  const uint4* wr = reinterpret_cast<const uint4*>(W + static_cast<size_t>(__ldcg(&rows[rank].target)) * K);
-  const float k = r * r / static_cast<float>(K) * c;
+  const float4 meta = __ldcg(reinterpret_cast<const float4*>(rows + rank));
+  const float r = meta.x, ut = __ldcg(u + rank);
+  const uint4* wr = reinterpret_cast<const uint4*>(W + static_cast<size_t>(__float_as_int(meta.w)) * K);
   const uint4* xr = reinterpret_cast<const uint4*>(x + static_cast<size_t>(row) * K);
-  for (int i = threadIdx.x; i < (K >> 3); i += 256) {
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-    for (int z = 0; z < planes; ++z) {
-      const float4* src = reinterpret_cast<const float4*>(acc + (static_cast<size_t>(z) * M + rank) * K) + 2 * i;
-      const float4 p = __ldcg(src), q = __ldcg(src + 1);
+  const float4* ar = reinterpret_cast<const float4*>(acc + static_cast<size_t>(rank) * K);
+  const size_t plane = static_cast<size_t>(M) * K / 4;
+  float4 a, b;
+  uint4 v, w;
+  auto load = [&](int i) {
+    a = __ldcg(ar + 2 * i), b = __ldcg(ar + 2 * i + 1);
+    v = __ldg(xr + i), w = __ldg(wr + i);
+  };
+  if (sub < chunks) load(sub);
+  float c = 0.f;
+#pragma unroll 4
+  for (int i = sub; i < parts; i += LPR) c += __ldcg(cpart + static_cast<size_t>(i) * M + rank);
+  c = warp_sum(c);
+  if (LPR > 32) {
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = c;
+    __syncthreads();
+    c = ((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7]));
+  }
+  const float k = r * r / static_cast<float>(K) * c;
+  for (int i = sub; i < chunks; i += LPR) {
+    if (i != sub) load(i);
+    for (int z = 1; z < planes; ++z) {
+      const float4 p = __ldcg(ar + z * plane + 2 * i), q = __ldcg(ar + z * plane + 2 * i + 1);
       a = make_float4(a.x + p.x, a.y + p.y, a.z + p.z, a.w + p.w);
       b = make_float4(b.x + q.x, b.y + q.y, b.z + q.z, b.w + q.w);
     }
-    const uint4 v = xr[i], w = __ldg(wr + i);
     a = make_float4(fmaf(ut, bf16lo_to_f32(w.x), a.x), fmaf(ut, bf16hi_to_f32(w.x), a.y), fmaf(ut, bf16lo_to_f32(w.y), a.z),
                     fmaf(ut, bf16hi_to_f32(w.y), a.w));
     b = make_float4(fmaf(ut, bf16lo_to_f32(w.z), b.x), fmaf(ut, bf16hi_to_f32(w.z), b.y), fmaf(ut, bf16lo_to_f32(w.w), b.z),

@@ -33,6 +33,8 @@ EPS = 1e-6
 SIZES = [
     (1, 8, 1), (1, 576, 49152), (3, 16, 5), (7, 64, 31), (16, 576, 33), (23, 576, 4099), (64, 136, 1000), (65, 1040, 257),
     (128, 64, 2049), (129, 576, 777), (257, 72, 3001), (300, 2056, 512), (517, 320, 8197),
+    # many rows per class (a pass of its own finishes dW*), also over 2048 rows, and just above that vocabulary
+    (2167, 280, 602), (2500, 64, 7), (1500, 2056, 130), (2600, 136, 2048), (2600, 136, 2056),
 ]
 
 
@@ -172,6 +174,20 @@ def test_masked_rows_hold_anything():
     dx, dW = fn.flashnorm_linear_cross_entropy_backward(g.cuda(), args[0], args[1], t.cuda(), lse, EPS)
     assert (loss == 0).all() and (dx == 0).all() and (dW == 0).all() and lse.isfinite().all()
     fn.flashnorm_check_device_error()
+
+
+@pytest.mark.parametrize("V", [1500, 5000])
+def test_one_frequent_class(V):
+    """Half of 700 rows share a class, as a frequent token does: more than the 32 that one look lists, in order; the sum is
+    the same whichever way dW* is finished."""
+    M, d = 700, 200
+    x, W, t, g = _draw(M, d, V, seed=11)
+    t[::2] = 33
+    _, lse, _, _, ctx = _forward(x, W, t, EPS, -100)
+    dx, dW = fn.flashnorm_linear_cross_entropy_backward(g.cuda(), x.cuda(), W.cuda(), t.cuda(), lse.float().cuda(), EPS)
+    want_dx, want_dW, t_dx, t_dW = _backward(g, lse.float(), ctx)
+    _near(dx, want_dx, t_dx, "dx")
+    _near(dW, want_dW, t_dW, "dW")
 
 
 def test_ignore_index_may_be_a_class():
