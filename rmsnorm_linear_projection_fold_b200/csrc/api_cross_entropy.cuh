@@ -69,15 +69,25 @@ int ce_mn_width(int64_t d) { return d > 128 ? 256 : 128; }
 // product cut into K ranges. With few rows the pass costs more than it saves (5 x 1080 x 1843: 9 us).
 constexpr int64_t kCeSmallVocab = 2048;
 
+// What an item of so many stages takes, in stages: at least its epilogue.
+int64_t ce_item_cost(int64_t kb) { return std::max<int64_t>(kb, 12); }
+
 // K ranges of a product that shares a launch with another: few enough planes, many enough items that the longest share of
 // any pair fits into an even part of both products' work.
 int ce_ksplit(const fn::PairGemmParams& g, const fn::PairGemmParams& other, int pairs) {
   const int64_t items = static_cast<int64_t>(g.num_m_tiles) * g.num_n_tiles;
-  const int64_t all = items * g.num_kb + static_cast<int64_t>(other.num_m_tiles) * other.num_n_tiles * other.num_kb;
+  const int64_t all = items * ce_item_cost(g.num_kb) + static_cast<int64_t>(other.num_m_tiles) * other.num_n_tiles * ce_item_cost(other.num_kb);
   const int64_t even = (all + pairs - 1) / pairs;
   int k = 1;
-  while (k < 64 && g.num_kb / (k + 1) >= 8 && (items * k + pairs - 1) / pairs * ((g.num_kb + k - 1) / k) > even) ++k;
+  while (k < 64 && g.num_kb / (k + 1) >= 8 &&
+         (items * k + pairs - 1) / pairs * ce_item_cost((g.num_kb + k - 1) / k) > even)
+    ++k;
   return k;
+}
+
+// Items of job 1 that take as long as one of job 0.
+int ce_extra(const fn::PairGemmParams& p, const fn::PairGemmParams& q) {
+  return static_cast<int>(std::max<int64_t>(1, ce_item_cost(p.num_kb / p.ksplit) / ce_item_cost(q.num_kb / q.ksplit)));
 }
 
 // Up to so many rows the loss streams W* past the tokens (cross_entropy_small.cuh).
@@ -332,7 +342,7 @@ fn_status flashnorm_linear_cross_entropy_backward(const void* g, const void* x, 
     using Dx = fn::PgJob<false, true, fn::CeDxEpi>;
     if (c.dw_ksplit) {
       q.ksplit = c.dw_ksplit;
-      q.extra = std::max(1, p.num_kb / p.ksplit / std::max(1, q.num_kb / q.ksplit));
+      q.extra = ce_extra(p, q);
       float* planes = reinterpret_cast<float*>(base + c.dw_acc);
       const fn::CeDxParams we = {planes, static_cast<int>(d), 0};
       st = launch_pair_gemm2<Dx, fn::PgJob<true, true, fn::CeDxEpi>>(ta, tb, p, xe, ta1, tb1, q, we, sms, dev, s, what);
@@ -342,13 +352,13 @@ fn_status flashnorm_linear_cross_entropy_backward(const void* g, const void* x, 
                         static_cast<int>(v0));
       if (e != cudaSuccess) return cuda_fail(e, "cross entropy dW launch");
     } else {
-      q.extra = std::max(1, p.num_kb / p.ksplit / q.num_kb);
+      q.extra = ce_extra(p, q);
       const fn::CeDwParams we = {live, xc, dWp, static_cast<int>(d), static_cast<int>(v0)};
       st = launch_pair_gemm2<Dx, fn::PgJob<true, true, fn::CeDwEpi>>(ta, tb, p, xe, ta1, tb1, q, we, sms, dev, s, what);
       if (st != FN_OK) return st;
     }
   }
-  const bool narrow = d <= 1024;  // a warp per row, else a block
+  const bool narrow = d / 8 * c.ksplit + parts <= 128;  // loads of a row: a warp for it, else a block
   e = launch_kernel(narrow ? fn::k_ce_dx<32> : fn::k_ce_dx<256>, dim3(static_cast<unsigned>(narrow ? (M + 7) / 8 : M)), dim3(256), 0, s,
                     1, static_cast<const float*>(acc), static_cast<const float*>(cpart), static_cast<const fn::CeRow*>(rows),
                     static_cast<const float*>(live.u), static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(Wstar),

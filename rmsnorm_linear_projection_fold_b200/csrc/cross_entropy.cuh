@@ -714,7 +714,7 @@ __global__ void __launch_bounds__(256) k_ce_dw(const float* __restrict__ acc, co
 }
 
 // dx[m, :] = sum of the planes + u[m] W*[t, :] - x[m, :] (r^2 / d) c[m], LPR threads per row; planes and partial sums c by
-// the row's rank among the live ones, in a fixed order. A thread's first 8 columns are on their way while c is summed.
+// the row's rank among the live ones, in a fixed order. A thread's first 16 columns are on their way while c is summed.
 template <int LPR>
 __global__ void __launch_bounds__(256) k_ce_dx(const float* __restrict__ acc, const float* __restrict__ cpart,
                                                const CeRow* __restrict__ rows, const float* __restrict__ u,
@@ -741,13 +741,19 @@ __global__ void __launch_bounds__(256) k_ce_dx(const float* __restrict__ acc, co
   const uint4* xr = reinterpret_cast<const uint4*>(x + static_cast<size_t>(row) * K);
   const float4* ar = reinterpret_cast<const float4*>(acc + static_cast<size_t>(rank) * K);
   const size_t plane = static_cast<size_t>(M) * K / 4;
-  float4 a, b;
-  uint4 v, w;
-  auto load = [&](int i) {
-    a = __ldcg(ar + 2 * i), b = __ldcg(ar + 2 * i + 1);
-    v = __ldg(xr + i), w = __ldg(wr + i);
+  constexpr int kAhead = 2;
+  float4 a[kAhead], b[kAhead];
+  uint4 v[kAhead], w[kAhead];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int h = 0; h < kAhead; ++h) {
+      const int i = i0 + h * LPR;
+      if (i >= chunks) break;
+      a[h] = __ldcg(ar + 2 * i), b[h] = __ldcg(ar + 2 * i + 1);
+      v[h] = __ldg(xr + i), w[h] = __ldg(wr + i);
+    }
   };
-  if (sub < chunks) load(sub);
+  load(sub);
   float c = 0.f;
 #pragma unroll 4
   for (int i = sub; i < parts; i += LPR) c += __ldcg(cpart + static_cast<size_t>(i) * M + rank);
@@ -758,21 +764,26 @@ __global__ void __launch_bounds__(256) k_ce_dx(const float* __restrict__ acc, co
     c = ((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7]));
   }
   const float k = r * r / static_cast<float>(K) * c;
-  for (int i = sub; i < chunks; i += LPR) {
-    if (i != sub) load(i);
-    for (int z = 1; z < planes; ++z) {
-      const float4 p = __ldcg(ar + z * plane + 2 * i), q = __ldcg(ar + z * plane + 2 * i + 1);
-      a = make_float4(a.x + p.x, a.y + p.y, a.z + p.z, a.w + p.w);
-      b = make_float4(b.x + q.x, b.y + q.y, b.z + q.z, b.w + q.w);
+  for (int i0 = sub; i0 < chunks; i0 += kAhead * LPR) {
+    if (i0 != sub) load(i0);
+#pragma unroll
+    for (int h = 0; h < kAhead; ++h) {
+      const int i = i0 + h * LPR;
+      if (i >= chunks) break;
+      float s[8] = {a[h].x, a[h].y, a[h].z, a[h].w, b[h].x, b[h].y, b[h].z, b[h].w};
+#pragma unroll 4
+      for (int z = 1; z < planes; ++z) {
+        const float4 p = __ldcg(ar + z * plane + 2 * i), q = __ldcg(ar + z * plane + 2 * i + 1);
+        s[0] += p.x, s[1] += p.y, s[2] += p.z, s[3] += p.w, s[4] += q.x, s[5] += q.y, s[6] += q.z, s[7] += q.w;
+      }
+      const uint32_t ww[4] = {w[h].x, w[h].y, w[h].z, w[h].w}, vv[4] = {v[h].x, v[h].y, v[h].z, v[h].w};
+      uint32_t o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        o[e] = pack_bf16x2(fmaf(-k, bf16lo_to_f32(vv[e]), fmaf(ut, bf16lo_to_f32(ww[e]), s[2 * e])),
+                           fmaf(-k, bf16hi_to_f32(vv[e]), fmaf(ut, bf16hi_to_f32(ww[e]), s[2 * e + 1])));
+      dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
     }
-    a = make_float4(fmaf(ut, bf16lo_to_f32(w.x), a.x), fmaf(ut, bf16hi_to_f32(w.x), a.y), fmaf(ut, bf16lo_to_f32(w.y), a.z),
-                    fmaf(ut, bf16hi_to_f32(w.y), a.w));
-    b = make_float4(fmaf(ut, bf16lo_to_f32(w.z), b.x), fmaf(ut, bf16hi_to_f32(w.z), b.y), fmaf(ut, bf16lo_to_f32(w.w), b.z),
-                    fmaf(ut, bf16hi_to_f32(w.w), b.w));
-    dst[i] = make_uint4(pack_bf16x2(fmaf(-k, bf16lo_to_f32(v.x), a.x), fmaf(-k, bf16hi_to_f32(v.x), a.y)),
-                        pack_bf16x2(fmaf(-k, bf16lo_to_f32(v.y), a.z), fmaf(-k, bf16hi_to_f32(v.y), a.w)),
-                        pack_bf16x2(fmaf(-k, bf16lo_to_f32(v.z), b.x), fmaf(-k, bf16hi_to_f32(v.z), b.y)),
-                        pack_bf16x2(fmaf(-k, bf16lo_to_f32(v.w), b.z), fmaf(-k, bf16hi_to_f32(v.w), b.w)));
   }
 }
 
