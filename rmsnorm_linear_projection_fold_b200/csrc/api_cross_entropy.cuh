@@ -16,7 +16,7 @@ fn_status make_mn_map(CUtensorMap* map, const void* ptr, int64_t cols, int64_t k
   return FN_OK;
 }
 
-// The same as blocks of 64 columns, cols % 64 == 0: boxes of `blocks` blocks x 64 k, one copy per stage (two copies took ...).
+// The same as blocks of 64 columns, cols % 64 == 0: boxes of `blocks` blocks x 64 k, one copy per stage.
 fn_status make_mn_block_map(CUtensorMap* map, const void* ptr, int64_t cols, int64_t k, int64_t ld, int blocks) {
   cuuint64_t dims[3] = {64u, static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(cols / 64)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, 128u};
@@ -59,7 +59,8 @@ struct CePlan {
   int64_t n_live, rows, rank_of, target, u, hits, xc, P, acc, dw_acc, bytes;  // backward (and part)
 };
 
-// Stages per accumulation of the forward's logits: 1024 k keep the drift of the tensor core's sums near 1e-6.
+// Stages per accumulation of the forward's logits: 1024 k. At k = 4096 the loss is then 3.4e-7 off (relative), 1.5e-6 with one
+// sum over all k; each accumulation of a tile costs about 650 cycles (2048 x 4096 x 32000: 376 against 361 us).
 constexpr int kCeFwdChunk = 16;
 
 // Tile width of the products whose B is MN-major (x or W*, [k][d]).

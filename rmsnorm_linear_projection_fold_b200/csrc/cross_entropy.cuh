@@ -4,9 +4,9 @@
 // The head is one more projection behind a norm, so the gain is folded into it and 1/rms deferred ("FlashNorm: Fast
 // Normalization for Transformers", Abstract): with r[m] = 1/sqrt(mean(x[m]^2) + eps),
 //     l[m, n] = r[m] sum_k x[m, k] W*[n, k],   lse[m] = log sum_n exp(l[m, n]),   loss[m] = lse[m] - l[m, t[m]].
-// Forward: the logits of a 256-row tile exist only in tensor memory; each epilogue thread owns a row and keeps the
-// running maximum and sum of exponentials of its columns, one (max, sum) pair per row, column tile and warp goes
-// to the workspace, and a second kernel joins them in a fixed order.
+// Forward (more than 64 rows; fewer: cross_entropy_small.cuh): the logits of a 256-row tile exist only in tensor memory;
+// each epilogue thread owns a row and keeps the running maximum and sum of exponentials of its columns, one (max, sum)
+// pair per row, column tile and warp goes to the workspace, and a second kernel joins them in a fixed order.
 // Backward: rows without a target have no gradient, so the live rows are packed first and only they go through the three
 // products (a batch half of prompt or padding costs half; what such rows hold cannot reach dW*). Then, in pieces of the
 // vocabulary, the logits are computed again and leave the chip as the factor both gradients share,
@@ -18,6 +18,11 @@
 // pass its rounding on to a whole row of dx and dW*: 0.0024 against 0.0017 relative, output rounding included. The other
 // entries' roundings, half a step of 2^-8 each, are independent and average out; tensor-core speed in both products
 // depends on them. Sums, c and the statistics are fp32.
+//
+// Measured at 2048 x 4096 x 32000 (each product 537 GFLOP): loss 335 us for the product, 12 around it; gradient, in two
+// pieces, packing 11, P 168 and both gradients' products 330 a piece, dx's last pass 21, together 1.04 ms for one call and
+// 1.25 back to back under the power cap (cuBLAS's rate there is 1.42 PFLOP/s: 1.13 ms for the products alone).
+// At 517 x 576 x 50257 (a tile of dW* has 8 stages of k): P 34, products 68 us, bound by the L2 and the epilogues.
 #pragma once
 
 #include "elementwise.cuh"

@@ -1,4 +1,5 @@
-// decode_int8.cuh — the 8-bit integer projection for at most 16 rows (decode), bound by the bytes of Q.
+// decode_int8.cuh — the 8-bit integer projection for at most 16 rows (decode), bound by the bytes of Q, behind a row pass:
+// for the shapes whose codes do not fit next to the ring of decode_int8_cluster.cuh.
 //
 // Operands swapped as in decode_tc.cuh: 128 rows of Q form the MMA's M side (kind::i8), the tokens its N side. The
 // contraction of each 128-row slab is cut into K ranges over independent CTAs, two on every SM, so that small

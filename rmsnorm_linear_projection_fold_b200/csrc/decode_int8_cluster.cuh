@@ -6,7 +6,11 @@
 // takes the partial maximum and sum of squares of every row, exchanges them with its cluster (distributed shared memory),
 // and writes the codes of its range straight into the MMA's operand layout. Partial sums go to the rank that finishes
 // their token, again through distributed shared memory: no workspace and no second launch. Each slab's cluster reads all of
-// x (from L2), which pays while that is little next to Q's bytes and the codes of a range fit beside the ring.
+// x from L2, at most a quarter of its Q bytes.
+//
+// Measured (warm): 1 x 576 -> 960 6.8 us (row pass and separate product: 4.5 + 7.8), all latency: launch, x, the exchange, the
+// MMAs' commit, the second exchange. 4 x 4096 -> 12288 15 us, of which Q's 50 MB need 7.8: the ring holds a third of Q while
+// the codes are made, the rest streams after.
 //
 // Warps: 0 = TMA producer, 1 = tensor memory + MMA issuer, 2..9 = quantization, then epilogue (two per lane quarter).
 #pragma once

@@ -11,7 +11,8 @@
 //
 // Operands. bf16 (kind::f16, fp32 accumulator) or int8 (kind::i8, exact int32 accumulator); a stage holds 128
 // bytes of K per row (64 bf16, 128 int8). A bf16 operand may also be "MN-major": stored [K][rows], as a
-// transposed factor of a gradient is; its stage is boxes of 64 k x 64 rows, each 64 lines of 128 bytes. Tiles of an
+// transposed factor of a gradient is; its stage is two boxes of 64 k x 64 rows, each 64 lines of 128 bytes, brought by one
+// copy where the rows are whole blocks of 64 (dx and dW* at 2048 x 4096 x 16000: 340 us, 370 with a copy per box). Tiles of an
 // MN-major B are multiples of 128 wide, so that every box starts on a 128-byte line: boxes that start in the middle of one
 // took 1.8 times as long (517 x 576 outputs, k = 50257: 125 against 69 us with narrower, aligned tiles). The last column
 // tile is only as wide as its columns need.
@@ -24,8 +25,15 @@
 // which it adds in its own registers.
 //
 // Warps: 0 = TMA producer, 1 = MMA issuer (leader) and tensor memory, the others epilogue, Epi::kParts (2 or 4) per lane
-// quarter. Four hide an epilogue's latencies better where a tile is short (the head's P at k = 576: ... us with two) and
-// leave each thread 112 registers instead of 168.
+// quarter. Four hide an epilogue's latencies better and leave each thread 96 registers instead of 168: the loss needs little
+// else (23 rows x 576 x 49152: 23 us with four, 26 with two), P's epilogue spills with four (170 us against 165 at 2048 x
+// 4096 x 16000).
+//
+// What bounds it: the tensor pipe, 86 % of cycles busy at 2048 x 4096 x 16000 (the clock then falls to 1.55 GHz: 1.6 PFLOP/s
+// for one launch, 1.3 back to back under the power cap); the L2 at k of a few stages or narrow tiles. One warp issues loads
+// and one MMAs, whole warps whose lane 0 issues, because both have little time: addresses and descriptors are offsets from
+// bases taken once per item, and placing the items in one thread, with its divisions, had cost 13 % (8-bit 2048 x 4096 x
+// 22016: 133 against 117 us).
 #pragma once
 
 #include <type_traits>
