@@ -70,6 +70,7 @@ _LIB_PATH = os.path.join(_PKG_DIR, "libflashnorm.so")
 FN_OK, FN_ERR_INVALID_ARG, FN_ERR_UNSUPPORTED, FN_ERR_ALIGN, FN_ERR_CUDA, FN_ERR_TIMEOUT = range(6)
 FN_BF16, FN_F32 = 0, 1
 NOALLOC_MAX_ELEMS = 1 << 23  # FN_NOALLOC_MAX_ELEMS in include/flashnorm.h
+_DTYPE_CODES = {torch.bfloat16: FN_BF16, torch.float32: FN_F32}
 PATHS = {"auto": 0, "tensor": 1, "gemv": 2, "decode": 3, "pair": 4}
 
 _P = ctypes.c_void_p
@@ -164,7 +165,7 @@ def _same_device(lead: torch.Tensor, **others) -> None:
     """Every tensor of a call must live on the device of `lead` (the C ABI takes bare pointers)."""
     ld = lead.get_device()  # the CUDA device index, or -1 for any other device (compared in full below)
     for name, t in others.items():
-        if t is not None and (ld < 0 or t.get_device() != ld) and t.device != lead.device:
+        if t is not None and (t.get_device() != ld or ld < 0) and t.device != lead.device:
             raise ValueError(f"{name} is on {t.device}, expected {lead.device}")
 
 
@@ -282,6 +283,9 @@ def prepare(func, *args, **kwargs) -> PreparedCall:
 
 
 def _need(t: torch.Tensor, name: str, dtype=torch.bfloat16, dim=None) -> None:
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous() and (
+            dim is None or t.dim() == dim):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -304,7 +308,7 @@ def _out_code(out_dtype) -> int:
 
 def _output(out, shape, dtype, like):
     if out is None:
-        return like.new_empty(shape, dtype=dtype)
+        return like.new_empty(shape) if dtype is like.dtype else like.new_empty(shape, dtype=dtype)
     _need(out, "out", dtype)
     if tuple(out.shape) != tuple(shape):
         raise ValueError(f"out must have shape {tuple(shape)}, got {tuple(out.shape)}")
@@ -661,7 +665,8 @@ def flashnorm_rope(x: torch.Tensor, rope_cs: torch.Tensor, positions: torch.Tens
         raise TypeError("x must be a torch.Tensor")
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
-    if x.dtype not in (torch.bfloat16, torch.float32):
+    code = _DTYPE_CODES.get(x.dtype)
+    if code is None:
         raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
     if x.dim() != 3:
         raise ValueError(f"x must be [M, H, head_dim], got shape {tuple(x.shape)}")
@@ -673,22 +678,31 @@ def flashnorm_rope(x: torch.Tensor, rope_cs: torch.Tensor, positions: torch.Tens
         raise ValueError("rope_cs must be [max_pos, rot_dim / 2, 2]")
     if positions.shape[0] != M:
         raise ValueError("positions must have one entry per row of x")
-    if layout not in ROPE_LAYOUTS:
+    pairs = ROPE_LAYOUTS.get(layout)
+    if pairs is None:
         raise ValueError('layout must be "interleaved" or "half"')
-    if x.stride(2) != 1 and hd > 1:
+    xs_row, xs_head, one = x.stride()
+    if one != 1 and hd > 1:
         raise ValueError("the features of a head must be contiguous")
+    ys_row, ys_head = xs_row, xs_head
     if out is None:
-        out = x.new_empty((M, H, hd))
+        if xs_head == hd and xs_row == H * hd:
+            out = torch.empty_like(x)
+        else:
+            out = x.new_empty((M, H, hd))
+            ys_row, ys_head = H * hd, hd
     elif out is not x:
         if not isinstance(out, torch.Tensor) or out.dtype != x.dtype:
             raise TypeError(f"out must be a {x.dtype} tensor")
         if out.shape != x.shape or (out.stride(2) != 1 and hd > 1):
             raise ValueError("out must have the shape of x, with contiguous features")
-    _same_device(x, rope_cs=rope_cs, positions=positions, out=out)
-    _invoke("flashnorm_rope", x, _ptr(x), _ptr(rope_cs), _ptr(positions), _ptr(out), M, H, hd, 2 * half,
-            H if n_rope_heads is None else int(n_rope_heads), max_pos, x.stride(0), x.stride(1), out.stride(0),
-            out.stride(1), ROPE_LAYOUTS[layout], int(bool(backward)), FN_BF16 if x.dtype == torch.bfloat16 else FN_F32,
-            _stream_ptr(x))
+        ys_row, ys_head = out.stride()[:2]
+        _same_device(x, out=out)
+    _same_device(x, rope_cs=rope_cs, positions=positions)
+    dev = x.get_device()
+    _invoke_on(dev, "flashnorm_rope", _ptr(x), _ptr(rope_cs), _ptr(positions), _ptr(out), M, H, hd, 2 * half,
+               H if n_rope_heads is None else int(n_rope_heads), max_pos, xs_row, xs_head, ys_row, ys_head, pairs,
+               1 if backward else 0, code, _stream_ptr(x))
     return out
 
 

@@ -16,26 +16,33 @@ int int8_ksplit(int64_t n_rows, int64_t d, int sms) {
 // How the one-launch decode kernel runs a shape; ranks 0: it does not (the codes of a K range leave too little shared
 // memory for the ring, at large d with so many slabs that few ranks fit).
 struct Int8Cluster {
-  int slabs, ranks, max_kb, stages;
+  int slabs, rows, ranks, max_kb, stages;
 };
 
 Int8Cluster int8_cluster_plan(int64_t M, int64_t d, int64_t n_rows, int sms) {
   Int8Cluster c = {};
   if (M > FN_DECODE_MAX_M) return c;
   const int64_t num_kb = (d + 127) / 128;
-  const int64_t slabs = (n_rows + fn::kI8Rows - 1) / fn::kI8Rows;
-  // a power of two of ranks that fits two CTAs per SM: clusters of 3 leave SMs empty and run in two waves (N = 12288,
-  // d = 4096: 22 us with 3, 15 with 2, 20 with 1 or, in two waves, 4)
-  int64_t ranks = 1;
-  while (2 * ranks <= std::min<int64_t>({2 * sms / slabs, num_kb, fn::kI8cMaxRanks})) ranks *= 2;
+  // rows of a slab and ranks (a power of two) that fill the most of two CTAs per SM: N = 12288, d = 4096 takes 128 slabs of
+  // 96 rows with 2 ranks. Clusters of 3 leave SMs empty and run in two waves (22 us with 3 ranks of 128 rows there, 15 with 2,
+  // 20 with 1 or, in two waves, 4).
+  int64_t rows = fn::kI8Rows, ranks = 1, slabs = 0, best = -1;
+  for (int64_t r = fn::kI8Rows; r >= 32; r -= 32) {
+    const int64_t n = (n_rows + r - 1) / r;
+    int64_t k = 1;
+    while (2 * k <= std::min<int64_t>({2 * sms / n, num_kb, fn::kI8cMaxRanks})) k *= 2;
+    const int64_t filled = n * k <= 2 * sms ? n * k : 0;  // more than one wave: only as whole slabs of 128
+    if (filled > best) rows = r, ranks = k, slabs = n, best = filled;
+  }
   const int64_t max_kb = (num_kb + ranks - 1) / ranks;
   // two CTAs per SM where the grid needs them (1 KB of each CTA's share is the system's)
   const int64_t budget = slabs * ranks <= sms ? 227 * 1024 : 228 * 1024 / 2 - 1024;
   if (max_kb > 256) return c;
-  const int64_t rest = budget - fn::int8_cluster_smem_bytes(static_cast<int>(M), static_cast<int>(max_kb), 0);
-  const int64_t stages = std::min<int64_t>({rest / fn::kI8WStage, max_kb, 16});
+  const int64_t rest = budget - fn::int8_cluster_smem_bytes(static_cast<int>(M), static_cast<int>(max_kb), 0, static_cast<int>(rows));
+  const int64_t stages = std::min<int64_t>({rest / (rows * 128), max_kb, 16});
   if (stages < std::min<int64_t>(max_kb, 3)) return c;
   c.slabs = static_cast<int>(slabs);
+  c.rows = static_cast<int>(rows);
   c.ranks = static_cast<int>(ranks);
   c.max_kb = static_cast<int>(max_kb);
   c.stages = static_cast<int>(stages);
@@ -105,7 +112,7 @@ fn_status launch_int8_cluster(const CUtensorMap& tw, const fn::Int8ClusterParams
     configured[dev] = true;
   }
   cudaError_t e = launch_kernel(kern, dim3(static_cast<unsigned>(slabs * p.ranks)), dim3(fn::kI8cThreads),
-                                fn::int8_cluster_smem_bytes(p.M, p.max_kb, p.stages), s, p.ranks, tw, p);
+                                fn::int8_cluster_smem_bytes(p.M, p.max_kb, p.stages, p.rows), s, p.ranks, tw, p);
   if (e != cudaSuccess) return cuda_fail(e, "int8 cluster decode launch");
   return FN_OK;
 }
@@ -131,7 +138,7 @@ fn_status run_int8(const void* x, const void* Q, const void* scales, void* y, in
   const Int8Cluster c = int8_cluster_plan(M, d, n_rows, sms);
   if (c.ranks) {
     CUtensorMap tw;
-    if ((st = make_u8_map(&tw, Q, d, n_rows, fn::kI8Rows)) != FN_OK) return st;
+    if ((st = make_u8_map(&tw, Q, d, n_rows, c.rows)) != FN_OK) return st;
     fn::Int8ClusterParams p;
     p.x = static_cast<const uint16_t*>(x);
     p.y = y;
@@ -142,6 +149,7 @@ fn_status run_int8(const void* x, const void* Q, const void* scales, void* y, in
     p.n_rows = static_cast<int>(n_rows);
     p.n_out = static_cast<int>(N);
     p.ranks = c.ranks;
+    p.rows = c.rows;
     p.stages = c.stages;
     p.max_kb = c.max_kb;
     p.eps = eps;

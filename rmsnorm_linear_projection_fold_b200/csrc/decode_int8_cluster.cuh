@@ -1,8 +1,9 @@
 // decode_int8_cluster.cuh — the 8-bit integer projection for at most 16 rows in one launch: the rows are quantized by the
 // CTAs that multiply them.
 //
-// As in decode_int8.cuh, 128 rows of Q form the MMA's M side and the tokens its N side, and the contraction of a 128-row
-// slab is cut into K ranges; here the ranges of a slab are the CTAs of a cluster. Each reads only its own K range of x,
+// As in decode_int8.cuh, rows of Q form the MMA's M side and the tokens its N side, and the contraction of a slab of rows is
+// cut into K ranges. A slab has 128 rows, or 96, 64 or 32 (the MMA's other rows are not used) where that fills more of the
+// SMs' two places each; here the ranges of a slab are the CTAs of a cluster. Each reads only its own K range of x,
 // takes the partial maximum and sum of squares of every row, exchanges them with its cluster (distributed shared memory),
 // and writes the codes of its range straight into the MMA's operand layout. Partial sums go to the rank that finishes
 // their token, again through distributed shared memory: no workspace and no second launch. Each slab's cluster reads all of
@@ -31,6 +32,7 @@ struct Int8ClusterParams {
   int n_rows;  // rows of Q
   int n_out;   // output columns
   int ranks;   // CTAs per slab
+  int rows;    // of a slab: a multiple of 32, at most 128
   int stages;  // of the ring
   int max_kb;  // of a rank
   float eps;
@@ -39,8 +41,9 @@ struct Int8ClusterParams {
 
 // Per K block: 8 rows of codes for at most 8 tokens, else 16.
 __host__ __device__ constexpr int int8_cluster_code_bytes(int M) { return M <= 8 ? 1024 : 2048; }
-__host__ __device__ constexpr int int8_cluster_smem_bytes(int M, int max_kb, int stages) {
-  return 1024 + stages * kI8WStage + max_kb * int8_cluster_code_bytes(M) + kI8cRedSlots * 512 + 2560;
+// The MMA reads 128 rows whatever the slab has: the codes (16 KB at most past the last stage's start) or what follows them.
+__host__ __device__ constexpr int int8_cluster_smem_bytes(int M, int max_kb, int stages, int rows) {
+  return 1024 + stages * rows * 128 + (kI8Rows - rows) * 128 + max_kb * int8_cluster_code_bytes(M) + kI8cRedSlots * 512 + 2560;
 }
 
 // Load 8 consecutive 32-bit columns of this thread's lane.
@@ -65,7 +68,8 @@ __global__ void __launch_bounds__(kI8cThreads, 2)
   uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
   const int code_bytes = int8_cluster_code_bytes(p.M);
   uint8_t* sW = smem;
-  uint8_t* sX = sW + p.stages * kI8WStage;
+  const int stage_bytes = p.rows * 128;
+  uint8_t* sX = sW + p.stages * stage_bytes;
   int* red = reinterpret_cast<int*>(sX + p.max_kb * code_bytes);            // [rank][token of mine][128]
   uint2* stat = reinterpret_cast<uint2*>(red + kI8cRedSlots * 128);         // [rank][16]: magnitude bits, sum of squares
   float* rho = reinterpret_cast<float*>(stat + kI8cMaxRanks * 16);          // [16]
@@ -82,7 +86,7 @@ __global__ void __launch_bounds__(kI8cThreads, 2)
   const int lane = static_cast<int>(threadIdx.x) & 31;
   const int ranks = p.ranks;
   const int slab = static_cast<int>(blockIdx.x) / ranks, rank = static_cast<int>(blockIdx.x) % ranks;
-  const int n0 = slab * kI8Rows;
+  const int n0 = slab * p.rows;
   const int kb0 = rank * p.num_kb / ranks, kb1 = (rank + 1) * p.num_kb / ranks;
 
   if (threadIdx.x == 0) {
@@ -115,8 +119,8 @@ __global__ void __launch_bounds__(kI8cThreads, 2)
     bool ok = true;
     const int first = min(kb1, kb0 + p.stages);
     auto load = [&]() {
-      mbar_arrive_expect_tx(&full[s], kI8WStage);
-      tma_load_2d(sW + s * kI8WStage, &tm_w, &full[s], kb * 128, n0);
+      mbar_arrive_expect_tx(&full[s], stage_bytes);
+      tma_load_2d(sW + s * stage_bytes, &tm_w, &full[s], kb * 128, n0);
     };
     auto advance = [&]() {
       if (++s == p.stages) {
@@ -181,7 +185,7 @@ __global__ void __launch_bounds__(kI8cThreads, 2)
           break;
         }
         tc_fence_after_sync();
-        const uint64_t da = make_sdesc_sw128(a0 + s * kI8WStage);
+        const uint64_t da = make_sdesc_sw128(a0 + s * stage_bytes);
         const uint64_t db = make_sdesc_sw128(b0 + (kb - kb0) * code_bytes);
 #pragma unroll
         for (int k = 0; k < 4; ++k)  // MMA k of every stage into accumulator k: four independent chains
@@ -308,10 +312,10 @@ __global__ void __launch_bounds__(kI8cThreads, 2)
     bool bad = false;
     for (int r = 0; r < ranks; ++r) bad |= failed[r] != 0;
     // a sum that a failed wait left incomplete is written as NaN (the status word reports the timeout)
-    const float sc = bad ? __int_as_float(0x7fc00000) : n < p.n_rows ? __ldg(p.scale + n) : 0.f;
+    const float sc = bad ? __int_as_float(0x7fc00000) : row < p.rows && n < p.n_rows ? __ldg(p.scale + n) : 0.f;
     // rows 32b + j (gate) and 32b + 16 + j (up) are lanes j and j + 16 of one warp
     const int col = GLU ? ((n0 + q * 32) >> 1) + (lane & 15) : n;
-    const bool mine = col < p.n_out && (!GLU || lane < 16);
+    const bool mine = row < p.rows && col < p.n_out && (!GLU || lane < 16);
     const int per = (kI8Tok + ranks - 1) / ranks;
     for (int i = half; i * ranks + rank < p.M; i += 2) {
       const int m = i * ranks + rank;
