@@ -758,9 +758,12 @@ _int8_ws_bytes_cache = {}
 
 def flashnorm_int8_workspace_bytes(M: int, d: int, N: int, glu: bool = False, device=None) -> int:
     """Workspace bytes flashnorm_linear_int8 (glu: flashnorm_glu_int8, with N = F) needs for this shape on `device`."""
-    dev = torch.cuda.current_device() if device is None else torch.device(device).index
-    if dev is None:
-        dev = torch.cuda.current_device()
+    if type(device) is int:
+        dev = device
+    else:
+        dev = torch.cuda.current_device() if device is None else torch.device(device).index
+        if dev is None:
+            dev = torch.cuda.current_device()
     key = (dev, M, d, N, glu)
     hit = _int8_ws_bytes_cache.get(key)
     if hit is not None:
@@ -787,17 +790,26 @@ def _call_workspace(workspace, nbytes: int, x: torch.Tensor):
     return workspace
 
 
-def _int8_call(x, Q, scales, glu):
+def _int8_call(entry, x, Q, scales, eps, out_dtype, out, glu, extra, workspace):
     _need(x, "x", dim=2)
     _need(Q, "Q", torch.int8, dim=2)
     _need(scales, "scales", torch.float32, dim=1)
     M, d = x.shape
-    rows = Q.shape[0]
-    if Q.shape[1] != d or scales.shape[0] != rows or (glu and rows % 2):
+    rows, dq = Q.shape
+    if dq != d or scales.shape[0] != rows or (glu and rows % 2):
         raise ValueError("Q [2F, d] and scales [2F] must match x [M, d]" if glu else
                          "Q [N, d] and scales [N] must match x [M, d]")
     _same_device(x, Q=Q, scales=scales)
-    return M, d, rows // 2 if glu else rows
+    code = _out_code(out_dtype)
+    N = rows // 2 if glu else rows
+    y = _output(out, (M, N), out_dtype, x)
+    if M == 0:
+        return y
+    dev = x.get_device()
+    ws = _call_workspace(workspace, flashnorm_int8_workspace_bytes(M, d, N, glu, dev), x)
+    _invoke_on(dev, entry, _ptr(x), _ptr(Q), _ptr(scales), _ptr(y), M, d, N, float(eps), *extra, code, _ptr(ws),
+               0 if ws is None else ws.numel(), _stream_ptr(x))
+    return y
 
 
 def flashnorm_linear_int8(x: torch.Tensor, Q: torch.Tensor, scales: torch.Tensor, eps: float,
@@ -806,28 +818,14 @@ def flashnorm_linear_int8(x: torch.Tensor, Q: torch.Tensor, scales: torch.Tensor
     flashnorm_fold_weights_int8, the product exact in int32, rho the row's scale times 1/rms (norm=False: without
     1/rms, for a projection that no norm precedes). workspace: "auto", or a uint8 CUDA tensor of at least
     flashnorm_int8_workspace_bytes(M, d, N) bytes."""
-    M, d, N = _int8_call(x, Q, scales, False)
-    y = _output(out, (M, N), out_dtype, x)
-    if M == 0:
-        return y
-    ws = _call_workspace(workspace, flashnorm_int8_workspace_bytes(M, d, N, False, x.get_device()), x)
-    _invoke("flashnorm_linear_int8", x, _ptr(x), _ptr(Q), _ptr(scales), _ptr(y), M, d, N, float(eps), int(bool(norm)),
-            _out_code(out_dtype), _ptr(ws), ws.numel() if ws is not None else 0, _stream_ptr(x))
-    return y
+    return _int8_call("flashnorm_linear_int8", x, Q, scales, eps, out_dtype, out, False, (1 if norm else 0,), workspace)
 
 
 def flashnorm_glu_int8(x: torch.Tensor, Q_gu: torch.Tensor, scales: torch.Tensor, eps: float,
                        out_dtype=torch.bfloat16, out=None, workspace="auto") -> torch.Tensor:
     """y = silu(gate) * up [M, F] in 8-bit integers (see flashnorm_linear_int8); Q_gu int8 [2F, d] and scales [2F] from
     flashnorm_fold_weights_int8(glu=True)."""
-    M, d, F = _int8_call(x, Q_gu, scales, True)
-    y = _output(out, (M, F), out_dtype, x)
-    if M == 0:
-        return y
-    ws = _call_workspace(workspace, flashnorm_int8_workspace_bytes(M, d, F, True, x.get_device()), x)
-    _invoke("flashnorm_glu_int8", x, _ptr(x), _ptr(Q_gu), _ptr(scales), _ptr(y), M, d, F, float(eps),
-            _out_code(out_dtype), _ptr(ws), ws.numel() if ws is not None else 0, _stream_ptr(x))
-    return y
+    return _int8_call("flashnorm_glu_int8", x, Q_gu, scales, eps, out_dtype, out, True, (), workspace)
 
 
 _ce_ws_bytes_cache = {}
@@ -835,9 +833,12 @@ _ce_ws_bytes_cache = {}
 
 def flashnorm_cross_entropy_workspace_bytes(M: int, d: int, V: int, backward: bool = False, device=None) -> int:
     """Workspace bytes flashnorm_linear_cross_entropy (or its backward) needs for this shape on `device`."""
-    dev = torch.cuda.current_device() if device is None else torch.device(device).index
-    if dev is None:
-        dev = torch.cuda.current_device()
+    if type(device) is int:
+        dev = device
+    else:
+        dev = torch.cuda.current_device() if device is None else torch.device(device).index
+        if dev is None:
+            dev = torch.cuda.current_device()
     key = (dev, M, d, V, backward)
     hit = _ce_ws_bytes_cache.get(key)
     if hit is not None:
@@ -872,11 +873,11 @@ def flashnorm_linear_cross_entropy(x: torch.Tensor, Wstar: torch.Tensor, targets
     flashnorm_cross_entropy_workspace_bytes(M, d, V) bytes."""
     M, d, V = _ce_call(x, Wstar, targets)
     loss = x.new_empty(M, dtype=torch.float32)
-    lse = x.new_empty(M, dtype=torch.float32)
+    lse = torch.empty_like(loss)
     if M == 0:
         return loss, lse
     ws = _call_workspace(workspace, flashnorm_cross_entropy_workspace_bytes(M, d, V, False, x.get_device()), x)
-    _invoke("flashnorm_linear_cross_entropy", x, _ptr(x), _ptr(Wstar), _ptr(targets), _ptr(loss), _ptr(lse), M, d, V,
+    _invoke_on(x.get_device(), "flashnorm_linear_cross_entropy", _ptr(x), _ptr(Wstar), _ptr(targets), _ptr(loss), _ptr(lse), M, d, V,
             float(eps), int(ignore_index), _ptr(ws), ws.numel() if ws is not None else 0, _stream_ptr(x))
     return loss, lse
 
