@@ -177,15 +177,17 @@ def _invoke(entry: str, lead: torch.Tensor, *args, report: str | None = None) ->
 
 # While prepare() records, on its own thread: the library calls made (size queries excepted) and every
 # tensor whose address was taken, which the prepared call keeps alive. Thread-local, so that calls made by
-# other threads meanwhile run as usual; _recorders, the number of threads that record, spares all calls the
-# thread-local lookups while none does.
-_rec = threading.local()
-_rec_lock = threading.Lock()
-_recorders = 0
+# other threads meanwhile run as usual.
+class _Recorder(threading.local):
+    calls = None
+    keep = None
+
+
+_rec = _Recorder()
 
 
 def _recording():
-    return getattr(_rec, "calls", None) if _recorders else None
+    return _rec.calls
 
 
 _entries = {}  # the library's functions by name
@@ -193,11 +195,10 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.curre
 
 
 def _invoke_on(dev: int, entry: str, *args, report: str | None = None) -> None:
-    if _recorders:
-        calls = _recording()
-        if calls is not None and not entry.endswith("_workspace_bytes"):
-            calls.append((dev, entry, args, report or entry))
-            return
+    calls = _rec.calls
+    if calls is not None and not entry.endswith("_workspace_bytes"):
+        calls.append((dev, entry, args, report or entry))
+        return
     f = _entries.get(entry)
     if f is None:
         f = _entries[entry] = getattr(load_library(), entry)
@@ -225,10 +226,9 @@ def _ptr(t):
     """A tensor's device address for a void* argument (None passes NULL)."""
     if t is None:
         return None
-    if _recorders:
-        keep = getattr(_rec, "keep", None)
-        if keep is not None:
-            keep.append(t)
+    keep = _rec.keep
+    if keep is not None:
+        keep.append(t)
     return t.data_ptr()
 
 
@@ -262,16 +262,11 @@ def prepare(func, *args, **kwargs) -> PreparedCall:
     and any scratch the call chose (a workspace="auto" buffer is allocated here and kept)."""
     if _recording() is not None:
         raise RuntimeError("prepare() does not nest")
-    global _recorders
     rec, keep = [], []
     _rec.calls, _rec.keep = rec, keep
-    with _rec_lock:
-        _recorders += 1
     try:
         result = func(*args, **kwargs)
     finally:
-        with _rec_lock:
-            _recorders -= 1
         _rec.calls, _rec.keep = None, None
     if len(rec) != 1:
         raise ValueError(f"prepare() takes a call that makes one library call; this one made {len(rec)}")
