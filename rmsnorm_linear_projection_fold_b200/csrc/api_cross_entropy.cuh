@@ -95,13 +95,16 @@ int ce_extra(const fn::PairGemmParams& p, const fn::PairGemmParams& q) {
 constexpr int kCeSmallRows = 64;
 constexpr int kCeFwdParts = fn::CeFwdEpi<false>::kParts;
 
-constexpr int64_t kCePieceBytes = int64_t{64} << 20;  // of P, per piece
+// P of a piece: at most so many bytes, unless that were fewer than kCePieceMin columns, between which dx's sums (8 bytes read
+// and written per element) would weigh too much. At 2048 x 4096 x 32000 (two pieces) the gradient takes 1.18 ms, 1.24 with
+// half the bytes, 1.16 with room for all of P.
+constexpr int64_t kCePieceBytes = int64_t{64} << 20, kCePieceMin = 4096;
 
 CePlan ce_plan(int64_t M, int64_t d, int64_t V, bool backward, int sms) {
   CePlan c = {};
   c.piece = V, c.pieces = 1, c.ksplit = 1;
   if (backward) {
-    const int64_t cap = std::max<int64_t>(2048, kCePieceBytes / (2 * M) / 256 * 256);
+    const int64_t cap = std::max<int64_t>(kCePieceMin, kCePieceBytes / (2 * M) / 256 * 256);
     c.pieces = (V + cap - 1) / cap;
     c.piece = c.pieces == 1 ? V : round_up((V + c.pieces - 1) / c.pieces, 256);
     c.pieces = (V + c.piece - 1) / c.piece;

@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(256) k_row_rstd(const uint16_t* __restrict__ x
   float s0 = 0.f, s1 = 0.f;
 #pragma unroll 4
   for (int c = lane; c < (K >> 3); c += 32) {
-    const uint4 v = src[c];
+    const uint4 v = __ldcg(src + c);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(256) k_ce_pack(const uint16_t* __restrict__ x,
     const uint4* src = reinterpret_cast<const uint4*>(x + static_cast<size_t>(m) * K);
 #pragma unroll
     for (int i = 0; i < kHeld; ++i)
-      held[i] = lane + 32 * i < chunks ? __ldg(src + lane + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+      held[i] = lane + 32 * i < chunks ? __ldcg(src + lane + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
   };
   if (m0 < M) load_row(m0);
   int n = 0;
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(256) k_ce_pack(const uint16_t* __restrict__ x,
     }
 #pragma unroll 4
     for (int c = lane + 32 * kHeld; c < chunks; c += 32) {
-      const uint4 v = __ldg(src + c);
+      const uint4 v = __ldcg(src + c);
       dst[c] = v;
       take(v);
     }
@@ -755,7 +755,7 @@ __global__ void __launch_bounds__(256) k_ce_dx(const float* __restrict__ acc, co
       const int i = i0 + h * LPR;
       if (i >= chunks) break;
       a[h] = __ldcg(ar + 2 * i), b[h] = __ldcg(ar + 2 * i + 1);
-      v[h] = __ldg(xr + i), w[h] = __ldg(wr + i);
+      v[h] = __ldcg(xr + i), w[h] = __ldcg(wr + i);
     }
   };
   load(sub);

@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(256) k_ce_rows_small(const uint16_t* __restric
   uint64_t ss = 0, dot = 0;
 #pragma unroll 4
   for (int c = lane; c < (K >> 3); c += 32) {
-    const uint4 v = __ldg(xr + c), w = __ldg(wr + c);
+    const uint4 v = __ldcg(xr + c), w = __ldcg(wr + c);
     const uint32_t a[4] = {v.x, v.y, v.z, v.w}, b[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {

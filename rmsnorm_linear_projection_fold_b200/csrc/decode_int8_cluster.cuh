@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kI8cThreads, 2)
       src[h] = reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(row < p.M ? row : 0) * p.K + k0);
 #pragma unroll
       for (int i = 0; i < kHeld; ++i)
-        held[h][i] = row < p.M && lane + 32 * i < pieces ? __ldg(src[h] + lane + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+        held[h][i] = row < p.M && lane + 32 * i < pieces ? __ldcg(src[h] + lane + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
     }
     cluster_wait();
 #pragma unroll
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kI8cThreads, 2)
       auto take = [&](const uint4& v) { int8_take(v, s2, amax); };
 #pragma unroll
       for (int i = 0; i < kHeld; ++i) take(held[h][i]);
-      for (int c = lane + 32 * kHeld; c < pieces; c += 32) take(__ldg(src[h] + c));
+      for (int c = lane + 32 * kHeld; c < pieces; c += 32) take(__ldcg(src[h] + c));
       uint32_t am = max(amax & 0xFFFFu, amax >> 16);
       am = __reduce_max_sync(0xffffffffu, am);
       const float2 halves = unpack_f32x2(s2);
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kI8cThreads, 2)
       for (int i = 0; i < kHeld; ++i)
         if (lane + 32 * i < all) put(lane + 32 * i, held[h][i]);
       for (int c = lane + 32 * kHeld; c < all; c += 32)
-        put(c, c < pieces ? __ldg(src[h] + c) : make_uint4(0u, 0u, 0u, 0u));
+        put(c, c < pieces ? __ldcg(src[h] + c) : make_uint4(0u, 0u, 0u, 0u));
     }
     fence_proxy_async_smem();
     __syncwarp();

@@ -156,7 +156,8 @@ struct Int8Row {
 };
 
 // LPR threads per row, 256 / LPR rows per block; a thread keeps up to 4 x 8 elements of its row in registers, and a
-// longer row's remainder is read a second time (from L2). Also zeroes the `nzero` words at `zero`, the arrival
+// longer row's remainder is read a second time. x is read from L2, here and in the other row passes: the kernel before may
+// have written it in place, and its own reads may have left older lines in this SM's L1. Also zeroes the `nzero` words at `zero`, the arrival
 // counters of a decode kernel that follows.
 // Bound: instruction issue before HBM (2048 x 4096: 25 MB in 10.3 us, launch included; with a conversion and a check per
 // code, 14 us). More blocks per SM with fewer registers were slower (11 to 16 us).
@@ -184,11 +185,11 @@ __global__ void __launch_bounds__(256) k_int8_rows(const uint16_t* __restrict__ 
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) {
     const int c = sub + i * LPR;
-    held[i] = c < chunks ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+    held[i] = c < chunks ? __ldcg(src + c) : make_uint4(0u, 0u, 0u, 0u);
   }
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) take(held[i]);
-  for (int c = sub + kHeld * LPR; c < chunks; c += LPR) take(src[c]);
+  for (int c = sub + kHeld * LPR; c < chunks; c += LPR) take(__ldcg(src + c));
   uint32_t am = max(amax & 0xFFFFu, amax >> 16);
   const float2 halves = unpack_f32x2(s2);
   float ss = halves.x + halves.y;
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(256) k_int8_rows(const uint16_t* __restrict__ 
     const int c = sub + i * LPR;
     if (c < chunks) put(c, held[i]);
   }
-  for (int c = sub + kHeld * LPR; c < chunks; c += LPR) put(c, src[c]);
+  for (int c = sub + kHeld * LPR; c < chunks; c += LPR) put(c, __ldcg(src + c));
 }
 
 // ---------------------------------------------------------------------------------------------- epilogues

@@ -126,6 +126,32 @@ def test_gradient_matches_float64(M, d, V):
     fn.flashnorm_check_device_error()
 
 
+def test_pieces_of_the_vocabulary():
+    """A vocabulary that takes two pieces, the second not a whole number of tiles: 64 bits on the GPU, in norm and row by
+    row (a row or class left out, or counted twice, would be wholly wrong)."""
+    M, d, V = 4200, 72, 9001
+    x, W, t, g = _draw(M, d, V, seed=12)
+    args = [v.cuda() for v in (x, W, t)]
+    loss, lse = fn.flashnorm_linear_cross_entropy(*args, EPS)
+    dx, dW = fn.flashnorm_linear_cross_entropy_backward(g.cuda(), *args, lse, EPS)
+    xd, Wd, td = x.cuda().double(), W.cuda().double(), args[2]
+    r = 1 / torch.sqrt((xd * xd).mean(dim=1, keepdim=True) + EPS)
+    l = (xd * r) @ Wd.T
+    live = td != -100
+    want = torch.logsumexp(l, dim=1)
+    assert (lse.double() - want).abs().max() < 1e-5  # |l| < 32: 100 roundings of 2^-24 |l| at most
+    at = td.clamp(min=0)[:, None]
+    assert (loss.double() - torch.where(live, want - l.gather(1, at)[:, 0], 0.0)).abs().max() < 2e-5
+    dl = torch.exp(l - lse.double()[:, None]).scatter_add_(1, at, torch.full_like(at, -1, dtype=torch.float64))
+    dl *= torch.where(live, g.cuda().double(), 0.0)[:, None]
+    dn = dl @ Wd
+    want_dx = r * (dn - xd * r * (dn * xd * r).mean(dim=1, keepdim=True))
+    want_dW = dl.T @ (xd * r)
+    for got, want in ((dx, want_dx), (dW, want_dW)):
+        off, size = (got.double() - want).norm(dim=1), want.norm(dim=1)
+        assert off.norm() <= 2.0 ** -7 * size.norm() and (off <= 2.0 ** -6 * size + 1e-7 * size.max()).all()
+
+
 def test_gradient_matches_differences():
     """Directional derivatives of sum g loss, the definition's losses at +-h in 64 bits. Central differences with
     h = 1e-4 along a unit direction are off by h^2 / 6 of the third derivative and 2^-52 / h of the value, both
