@@ -12,7 +12,9 @@
  * before SiLU) and to RMSNorm -> linear -> RMSNorm, where the first norm is dropped by the scale
  * invariance of RMS (same abstract). The abstract also names LayerNorm, RoPE-based attention and
  * quantized models among the cases the technique carries over to; this library covers LayerNorm ->
- * linear, RoPE on the normalised heads of the post-norm path, and FP8 E4M3 weights for decode.
+ * linear, RoPE on the normalised heads of the post-norm path, FP8 E4M3 and NVFP4 weights for decode, and 8-bit
+ * integer weights and activations. Around the projections it has rotary positions on heads in memory and the cross
+ * entropy of the vocabulary head (one more projection behind a norm) with its gradient.
  *
  * Conventions shared by every entry point
  *   - All tensor pointers are caller-owned DEVICE memory on the current device; the library never
@@ -341,7 +343,8 @@ FN_API fn_status flashnorm_int8_workspace_bytes(int64_t M, int64_t d, int64_t N,
  * (the same Abstract items: the gain is folded into the head, 1/rms deferred):
  *     r[m] = 1/sqrt(mean(x[m]^2) + eps),   l[m][n] = r[m] sum_k x[m][k] W*[n][k]
  *     lse[m] = log sum_n exp(l[m][n]),     loss[m] = lse[m] - l[m][targets[m]]
- * flashnorm_linear_cross_entropy: x bf16 [M, d], Wstar bf16 [V, d] (flashnorm_fold_weights), targets int64 [M] ->
+ * flashnorm_linear_cross_entropy: x bf16 [M, d], Wstar bf16 [V, d] (flashnorm_fold_weights, or any such matrix with the
+ *   gain multiplied in: V itself needs no alignment), targets int64 [M] ->
  *   loss and lse, fp32 [M]. A row whose target is ignore_index has loss 0 (its lse is computed all the same). A target
  *   that is neither a class (0 .. V-1) nor ignore_index gives that row a NaN loss, and the next
  *   flashnorm_check_device_error returns FN_ERR_INVALID_ARG.
