@@ -352,7 +352,8 @@ FN_API fn_status flashnorm_int8_workspace_bytes(int64_t M, int64_t d, int64_t N,
  *   dx bf16 [M, d] and dWstar bf16 [V, d], both overwritten. With dl[m][n] = g[m] (exp(l[m][n] - lse[m]) - [n = t[m]]):
  *     dW*[n] = sum_m r[m] dl[m][n] x[m],   dx[m] = r[m] sum_n dl[m][n] W*[n] - x[m] (r[m]^2 / d) sum_n dl[m][n] l[m][n]
  *   Rows whose target is ignore_index have a zero dx and take no part in dW*; a bad target gives its row a NaN dx, takes
- *   no part in dW* and is reported as above. r dl is rounded to bf16 once for the two products; sums are fp32. M == 0
+ *   no part in dW* and is reported as above. r dl is rounded to bf16 once for the two products, but for the
+ *   target's own entry, which stays fp32 (for dW* not where a class is frequent); sums are fp32. M == 0
  *   sets dWstar to zero.
  * flashnorm_cross_entropy_workspace_bytes: the scratch a call (backward: 0 or 1) of this shape needs on the current
  *   device, written to *bytes; bounded by a piece of the vocabulary, not the whole. Caller-owned, 16-byte aligned,

@@ -66,7 +66,7 @@ constexpr int kCeFwdChunk = 16;
 // Tile width of the products whose B is MN-major (x or W*, [k][d]).
 int ce_mn_width(int64_t d) { return d > 128 ? 256 : 128; }
 
-// Up to so many classes, and with a row for every fourth at least, dW* is finished by a pass of its own (k_ce_dw), its
+// Up to so many classes, and with a row for every sixteenth at least, dW* is finished by a pass of its own (k_ce_dw), its
 // product cut into K ranges. With few rows the pass costs more than it saves (5 x 1080 x 1843: 9 us).
 constexpr int64_t kCeSmallVocab = 2048;
 
@@ -129,7 +129,7 @@ CePlan ce_plan(int64_t M, int64_t d, int64_t V, bool backward, int sms) {
   plan_pair_gemm_bn(&g, M, d, (c.piece + 63) / 64, ce_mn_width(d), 1);
   plan_pair_gemm_bn(&w, c.piece, d, (M + 63) / 64, ce_mn_width(d), 1);
   c.ksplit = ce_ksplit(g, w, sms / 2);
-  c.dw_ksplit = V <= kCeSmallVocab && 4 * M >= V ? ce_ksplit(w, g, sms / 2) : 0;
+  c.dw_ksplit = V <= kCeSmallVocab && 16 * M >= V ? ce_ksplit(w, g, sms / 2) : 0;
   const int64_t Mp = round_up(M, 64);  // the packed rows, zeros at their end
   c.n_live = 0;
   c.rows = 256;
@@ -324,7 +324,8 @@ fn_status flashnorm_linear_cross_entropy_backward(const void* g, const void* x, 
     p.N = static_cast<int>(width);
     p.num_n_tiles = static_cast<int>((width + p.bn - 1) / p.bn);
     p.live = n_live;
-    const fn::CeGradParams ge = {rows, P, cpart + static_cast<int64_t>(parts) * M, static_cast<int>(ldp), static_cast<int>(v0), live};
+    const fn::CeGradParams ge = {rows, P, cpart + static_cast<int64_t>(parts) * M, static_cast<int>(ldp), static_cast<int>(v0),
+                                 V > kCeSmallVocab ? 3 : 33, live};
     parts += fn::CeGradEpi::kParts * p.num_n_tiles;
     if ((st = make_k_map(&ta, xc, d, Mp, d, 128)) != FN_OK) return st;
     if ((st = make_k_map(&tb, W, d, width, d, p.bn / 2)) != FN_OK) return st;

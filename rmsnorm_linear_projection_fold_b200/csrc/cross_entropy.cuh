@@ -11,7 +11,8 @@
 // products (a batch half of prompt or padding costs half; what such rows hold cannot reach dW*). Then, in pieces of the
 // vocabulary, the logits are computed again and leave the chip as the factor both gradients share,
 //     P[m, n] = r[m] dl[m, n] in bf16,   dl[m, n] = g[m] (exp(l - lse) - [n = t]),
-// except for the target's own entry u[m] = r dl[m, t], which stays fp32 (P is 0 there):
+// except for the target's own entry u[m] = r dl[m, t], which stays fp32 (P is 0 there; in blocks of 32 rows where three
+// targets or more lie within 32 classes of a large vocabulary P has it rounded, and u is the rest, which dW* then leaves out):
 //     dW*[n, :] = sum_m P[m, n] x[m, :] + sum_{m: t[m] = n} u[m] x[m, :]
 //     dx[m, :]  = sum_n P[m, n] W*[n, :] + u[m] W*[t, :] - x[m, :] (r[m]^2 / d) c[m],   c[m] = sum_n dl[m, n] l[m, n]
 // (the last term is the norm's own share: dr/dx = -r^3 x / d). The target's entry is most of a row's gradient and would
@@ -247,8 +248,9 @@ struct __align__(16) CeRow {
 struct CeLive {
   const int* n_live;
   int* target;  // [live rows]
-  float* u;     // r dl of the target's entry
+  float* u;     // r dl of the target's entry, less what P has of it
   // [32 vocabulary columns of the piece][ld_hits: 32 live rows]: which of these rows have their target among these columns
+  // and its entry not in P
   unsigned* hits;
   int ld_hits;
 };
@@ -358,6 +360,7 @@ struct CeGradParams {
   float* cpart;    // [kParts column tiles][M] partial c, this piece's
   int ldp;         // a multiple of 64: rows of P start on whole 128-byte lines
   int v0;          // first column of the piece within the vocabulary
+  int often;       // targets in a block of 32 rows and 32 classes from which on P has them
   CeLive live;
 };
 
@@ -416,17 +419,25 @@ struct CeGradEpi {
       const int at = t0 - c0;
       const bool hit = row < t.M && at >= 0 && at < 32 && c0 + at < t.width;
       const unsigned hits = __ballot_sync(0xffffffffu, hit);
-      if (lane == 0) e.live.hits[static_cast<size_t>((t.n0 + c0) >> 5) * e.live.ld_hits + (t.row0 >> 5)] = hits;
-      if (hit) {  // the target's entry: kept in fp32, 0 in P
+      // `often` rows of the block or more: a frequent class, whose many entries' roundings average out. dW* takes them from P
+      // then, so that no warp of its epilogue has more than two rows in 32 to add by itself (2048 x 1024 x 32000 with a
+      // tenth of the rows, or all, of one class: 341 and 318 us; 496 and 2323 if all are added there; 326 with none).
+      const bool often = __popc(hits) >= e.often;
+      if (lane == 0) e.live.hits[static_cast<size_t>((t.n0 + c0) >> 5) * e.live.ld_hits + (t.row0 >> 5)] = often ? 0u : hits;
+      if (hit) {  // the target's entry: kept in fp32, 0 in P, or what its rounding in P leaves of it
         float z = 0.f;
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-          if (at == j) {
-            z = __uint_as_float(v[j >> 4][j & 15]);
-            if (j & 1) o[j >> 1].y = 0.f; else o[j >> 1].x = 0.f;
-          }
-        e.live.u[row] = gr * (ex2(fmaf(z, r2, q.nlse2)) - 1.0f);
+          if (at == j) z = __uint_as_float(v[j >> 4][j & 15]);
+        const float u = gr * (ex2(fmaf(z, r2, q.nlse2)) - 1.0f);
+        const float in_p = often ? bf16lo_to_f32(pack_bf16x2(u, 0.f) & 0xFFFFu) : 0.f;
+        e.live.u[row] = u - in_p;
         ct = -z;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (at == j) {
+            if (j & 1) o[j >> 1].y = in_p; else o[j >> 1].x = in_p;
+          }
       }
 #pragma unroll
       for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(o[j].x, o[j].y);

@@ -202,13 +202,14 @@ def test_masked_rows_hold_anything():
     fn.flashnorm_check_device_error()
 
 
+@pytest.mark.parametrize("every", [1, 2, 13])
 @pytest.mark.parametrize("V", [1500, 5000])
-def test_one_frequent_class(V):
-    """Half of 700 rows share a class, as a frequent token does: more than the 32 that one look lists, in order; the sum is
-    the same whichever way dW* is finished."""
+def test_one_frequent_class(V, every):
+    """Rows that share a class, as a frequent token's do: all, half, or two in most blocks of 32 (more than the 32 that one
+    look lists); right whichever way dW* is finished."""
     M, d = 700, 200
     x, W, t, g = _draw(M, d, V, seed=11)
-    t[::2] = 33
+    t[::every] = 33
     _, lse, _, _, ctx = _forward(x, W, t, EPS, -100)
     dx, dW = fn.flashnorm_linear_cross_entropy_backward(g.cuda(), x.cuda(), W.cuda(), t.cuda(), lse.float().cuda(), EPS)
     want_dx, want_dW, t_dx, t_dW = _backward(g, lse.float(), ctx)
