@@ -180,9 +180,9 @@ struct CeFwdEpi {
 };
 
 // lse and loss of a row by LANES consecutive lanes: each joins every LANES-th partial pair, then they join in a butterfly (a
-// fixed order). An ignored row's loss is 0; a target that is neither a class nor ignore_index gives NaN and is reported.
-// Every lane of the warp calls, live or not.
-template <int LANES>
+// fixed order). BATCH pairs of a lane are loaded at once. An ignored row's loss is 0; a target that is neither a class nor
+// ignore_index gives NaN and is reported. Every lane of the warp calls, live or not.
+template <int LANES, int BATCH>
 __device__ __forceinline__ void ce_join_row(const float2* part, int parts, const float* tlogit, const long long* targets,
                                             float* loss, float* lse, int row, bool live, int V, long long ignore, int lane) {
   const int sub = lane % LANES;
@@ -196,19 +196,19 @@ __device__ __forceinline__ void ce_join_row(const float2* part, int parts, const
     s = s * ex2(m - base) + qs * ex2(qm - base);
     m = mn;
   };
-  for (int i0 = sub; i0 < parts; i0 += 10 * LANES) {
-    float2 q[10];
+  for (int i0 = sub; i0 < parts; i0 += BATCH * LANES) {
+    float2 q[BATCH];
 #pragma unroll
-    for (int k = 0; k < 10; ++k)
+    for (int k = 0; k < BATCH; ++k)
       q[k] = live && i0 + k * LANES < parts ? __ldcg(src + i0 + k * LANES) : make_float2(-INFINITY, 0.f);
     // the batch's maximum first: one exponential a pair instead of two
     float mn = m;
 #pragma unroll
-    for (int k = 0; k < 10; ++k) mn = fmaxf(mn, q[k].x);
+    for (int k = 0; k < BATCH; ++k) mn = fmaxf(mn, q[k].x);
     const float base = mn == -INFINITY ? 0.f : mn;
     s *= ex2(m - base);
 #pragma unroll
-    for (int k = 0; k < 10; ++k) s = fmaf(q[k].y, ex2(q[k].x - base), s);
+    for (int k = 0; k < BATCH; ++k) s = fmaf(q[k].y, ex2(q[k].x - base), s);
     m = mn;
   }
 #pragma unroll
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(256) k_ce_join(const float2* __restrict__ part
   grid_dep_wait();
   grid_dep_launch();
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  ce_join_row<32>(part, parts, tlogit, targets, loss, lse, row, row < M, V, ignore, lane);
+  ce_join_row<32, 10>(part, parts, tlogit, targets, loss, lse, row, row < M, V, ignore, lane);
 }
 
 // ---------------------------------------------------------------------------------------------- backward

@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(kCsThreads, 1)
   constexpr int kTok = 2 * NT;
   constexpr int kWBytes = kCsRows * 128, kXBytes = kTok * 128;
   constexpr uint32_t kCols = kTok < 32 ? 32 : kTok;  // per accumulator
+  constexpr int kJoin = 256 / kTok;                  // lanes per token in the final join
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
@@ -300,9 +301,8 @@ __global__ void __launch_bounds__(kCsThreads, 1)
     if (threadIdx.x == 64) *arrival = atom_add_acq_rel_gpu(p.arrived, 1u);
     named_bar_sync(1, 256);
     if (*arrival == gridDim.x - 1)
-      for (int row0 = 0; row0 < p.M; row0 += 32)
-        ce_join_row<8>(p.part, parts, p.tlogit, p.targets, p.loss, p.lse, row0 + (tok >> 3), row0 + (tok >> 3) < p.M, p.V,
-                       p.ignore, lane);
+      // all tokens at once, 19 pairs of each lane in flight: every other SM is idle meanwhile
+      ce_join_row<kJoin, 19>(p.part, parts, p.tlogit, p.targets, p.loss, p.lse, tok / kJoin, tok / kJoin < p.M, p.V, p.ignore, lane);
   }
   tc_fence_before_sync();
   __syncthreads();
