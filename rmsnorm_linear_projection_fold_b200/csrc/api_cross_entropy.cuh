@@ -166,9 +166,9 @@ fn_status check_ce_call(const void* x, const void* w, const void* targets, const
   return check_ptr(workspace, "workspace");
 }
 
-fn_status launch_rstd(const void* x, float* rstd, int64_t M, int64_t d, float eps, cudaStream_t s) {
+fn_status launch_rstd(const void* x, float* rstd, unsigned* arrived, int64_t M, int64_t d, float eps, cudaStream_t s) {
   cudaError_t e = launch_kernel(fn::k_row_rstd, dim3(static_cast<unsigned>((M + 7) / 8)), dim3(256), 0, s, 1,
-                                static_cast<const uint16_t*>(x), rstd, static_cast<int>(M), static_cast<int>(d), eps);
+                                static_cast<const uint16_t*>(x), rstd, arrived, static_cast<int>(M), static_cast<int>(d), eps);
   return e == cudaSuccess ? FN_OK : cuda_fail(e, "row statistics launch");
 }
 
@@ -239,11 +239,7 @@ fn_status flashnorm_linear_cross_entropy(const void* x, const void* Wstar, const
     CUtensorMap tx, tw;
     if ((st = make_k_map(&tx, x, d, M, d, tokens)) != FN_OK) return st;
     if ((st = make_k_map(&tw, Wstar, d, V, d, fn::kCsRows)) != FN_OK) return st;
-    cudaError_t e = launch_kernel(fn::k_ce_rows_small, dim3(static_cast<unsigned>((M + 7) / 8)), dim3(256), 0, s, 1,
-                                  static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(Wstar), p.targets, rstd,
-                                  reinterpret_cast<float*>(base + c.tlogit), p.arrived, p.M, static_cast<int>(d), p.V, eps,
-                                  static_cast<long long>(ignore_index));
-    if (e != cudaSuccess) return cuda_fail(e, "cross entropy row pass launch");
+    if ((st = launch_rstd(x, rstd, p.arrived, M, d, eps, s)) != FN_OK) return st;
     return tokens == 16 ? launch_ce_small<8>(tw, tx, p, sms, dev, s)
                         : tokens == 32 ? launch_ce_small<16>(tw, tx, p, sms, dev, s) : launch_ce_small<32>(tw, tx, p, sms, dev, s);
   }
@@ -259,7 +255,7 @@ fn_status flashnorm_linear_cross_entropy(const void* x, const void* Wstar, const
   CUtensorMap tx, tw;
   if ((st = make_k_map(&tx, x, d, M, d, 128)) != FN_OK) return st;
   if ((st = make_k_map(&tw, Wstar, d, V, d, p.bn / 2)) != FN_OK) return st;
-  if ((st = launch_rstd(x, rstd, M, d, eps, s)) != FN_OK) return st;
+  if ((st = launch_rstd(x, rstd, nullptr, M, d, eps, s)) != FN_OK) return st;
   const char* what = "cross entropy GEMM";
   st = p.num_kb > kCeFwdChunk
            ? launch_pair_gemm<fn::PG_BF16, fn::PgJob<false, false, fn::CeFwdEpi<true>>>(tx, tw, p, ep, sms, dev, s, what)

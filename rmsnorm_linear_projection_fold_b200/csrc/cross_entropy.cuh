@@ -40,11 +40,13 @@ __device__ __forceinline__ float ex2(float v) {
   return e;
 }
 
-// r[m] = 1/sqrt(mean(x[m]^2) + eps), one warp per row.
-__global__ void __launch_bounds__(256) k_row_rstd(const uint16_t* __restrict__ x, float* __restrict__ rstd, int M, int K,
-                                                  float eps) {
+// r[m] = 1/sqrt(mean(x[m]^2) + eps), one warp per row. Also zeroes `arrived` (not null: the arrival counter of the kernel that
+// follows).
+__global__ void __launch_bounds__(256) k_row_rstd(const uint16_t* __restrict__ x, float* __restrict__ rstd,
+                                                  unsigned* __restrict__ arrived, int M, int K, float eps) {
   grid_dep_wait();
   grid_dep_launch();
+  if (arrived != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *arrived = 0u;
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (row >= M) return;
   const uint4* src = reinterpret_cast<const uint4*>(x + static_cast<size_t>(row) * K);

@@ -4,8 +4,10 @@
 // cost next to nothing and the kernel only streams W*, one persistent CTA per SM with a deep ring. An epilogue thread owns
 // one vocabulary row of each slab and half of the tokens; it keeps a running (maximum, sum) per token over all slabs of its
 // CTA. At the end the lanes of a warp join theirs (each exchange halves the tokens a lane holds), every CTA writes one pair
-// per token, and the last CTA to arrive joins all of them in a fixed order. One pass before it takes 1/rms, the target's
-// logit (a dot product of its own) and zeroes the arrival counter; W* and x do not depend on it and are fetched meanwhile.
+// per token, and the last CTA to arrive joins all of them in a fixed order. The pass before it takes 1/rms and zeroes the
+// arrival counter; W* and x do not depend on it and are fetched meanwhile, so it reads nothing but x: its loads queue behind
+// W*'s, and when it fetched the targets' rows of W* for their logits too, the epilogue waited for it (23 rows x 576 x
+// 49152, call after call: 18.4 us, 17.7 so). A target's logit is taken by the thread whose row it is.
 //
 // Bound: HBM. 23 x 576 x 49152: 16.8 us for 57 MB (8.7 at the copy rate): 4 to start, 3 a slab, 2.5 for the join (a warp per
 // token instead of 8 lanes: 6.4). The CTA-pair product, which spends 256 rows of MMA on them, takes 19.5 and a join of 5.
@@ -30,7 +32,7 @@ __host__ __device__ constexpr int ce_small_smem_bytes(int tokens) {
 
 struct CeSmallParams {
   const float* rstd;
-  const float* tlogit;
+  float* tlogit;      // [M]
   const long long* targets;
   float2* part;       // [M][CTAs]
   unsigned* arrived;  // zeroed by the pass before
@@ -39,40 +41,6 @@ struct CeSmallParams {
   int M, V, num_kb;
   long long ignore;
 };
-
-// 1/rms and the target's logit of each row, one warp per row.
-__global__ void __launch_bounds__(256) k_ce_rows_small(const uint16_t* __restrict__ x, const uint16_t* __restrict__ W,
-                                                       const long long* __restrict__ targets, float* __restrict__ rstd,
-                                                       float* __restrict__ tlogit, unsigned* __restrict__ arrived, int M,
-                                                       int K, int V, float eps, long long ignore) {
-  grid_dep_wait();
-  grid_dep_launch();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *arrived = 0u;
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row >= M) return;
-  const long long t = __ldg(targets + row);
-  const uint4* xr = reinterpret_cast<const uint4*>(x + static_cast<size_t>(row) * K);
-  const uint4* wr = reinterpret_cast<const uint4*>(W + static_cast<size_t>(t != ignore && target_is_class(t, V) ? t : 0) * K);
-  uint64_t ss = 0, dot = 0;
-#pragma unroll 4
-  for (int c = lane; c < (K >> 3); c += 32) {
-    const uint4 v = __ldcg(xr + c), w = __ldcg(wr + c);
-    const uint32_t a[4] = {v.x, v.y, v.z, v.w}, b[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint64_t p = pack_f32x2(bf16lo_to_f32(a[e]), bf16hi_to_f32(a[e]));
-      ss = fma_f32x2(p, p, ss);
-      dot = fma_f32x2(p, pack_f32x2(bf16lo_to_f32(b[e]), bf16hi_to_f32(b[e])), dot);
-    }
-  }
-  const float2 s2 = unpack_f32x2(ss), d2 = unpack_f32x2(dot);
-  const float s = warp_sum(s2.x + s2.y), d = warp_sum(d2.x + d2.y);
-  if (lane == 0) {
-    const float r = 1.0f / sqrtf(s / static_cast<float>(K) + eps);
-    rstd[row] = r;
-    tlogit[row] = r * d;
-  }
-}
 
 // NT: tokens per epilogue thread; the MMA has 2 NT.
 template <int NT>
@@ -220,6 +188,8 @@ __global__ void __launch_bounds__(kCsThreads, 1)
     // ------------------------------------------------------------------ epilogue
     const int w = warp - 2, q = warp & 3, half = w >> 2;
     grid_dep_wait();
+    // lane j: the target of the warp's token j
+    const long long target = lane < NT && half * NT + lane < p.M ? __ldg(p.targets + half * NT + lane) : -1;
     float r2[NT], m[NT], s[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -254,6 +224,16 @@ __global__ void __launch_bounds__(kCsThreads, 1)
         if (lane == 0) mbar_arrive(&acc_empty[acc]);
         acc ^= 1;
         if (acc == 0) acc_ph ^= 1u;
+      }
+      const long long row = target - (static_cast<long long>(slab) * kCsRows + q * 32);
+      for (unsigned hits = __ballot_sync(0xffffffffu, ok && row >= 0 && row < 32); hits != 0; hits &= hits - 1) {
+        const int j0 = __ffs(hits) - 1;
+        if (__shfl_sync(0xffffffffu, static_cast<int>(row), j0) != lane) continue;
+        float v = 0.f;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          if (j == j0) v = z[j];
+        p.tlogit[half * NT + j0] = v * __ldcg(p.rstd + half * NT + j0);
       }
       if (ok && slab * kCsRows + q * 32 + lane < p.V) {
 #pragma unroll
