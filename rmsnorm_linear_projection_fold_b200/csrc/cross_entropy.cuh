@@ -4,7 +4,7 @@
 // The head is one more projection behind a norm, so the gain is folded into it and 1/rms deferred ("FlashNorm: Fast
 // Normalization for Transformers", Abstract): with r[m] = 1/sqrt(mean(x[m]^2) + eps),
 //     l[m, n] = r[m] sum_k x[m, k] W*[n, k],   lse[m] = log sum_n exp(l[m, n]),   loss[m] = lse[m] - l[m, t[m]].
-// Forward (more than 64 rows; fewer: cross_entropy_small.cuh): the logits of a 256-row tile exist only in tensor memory;
+// Forward (more than 32 rows; fewer: cross_entropy_small.cuh): the logits of a 256-row tile exist only in tensor memory;
 // each epilogue thread owns a row and keeps the running maximum and sum of exponentials of its columns, one (max, sum)
 // pair per row, column tile and warp goes to the workspace, and a second kernel joins them in a fixed order.
 // Backward: rows without a target have no gradient, so the live rows are packed first and only they go through the three

@@ -1,4 +1,4 @@
-// cross_entropy_small.cuh — the vocabulary head's cross entropy for at most 64 rows, bound by the bytes of W*.
+// cross_entropy_small.cuh — the vocabulary head's cross entropy for at most 32 rows, bound by the bytes of W*.
 //
 // Operands swapped as in decode_tc.cuh: 128 rows of W* form the MMA's M side, the tokens its N side, so that a slab's MMAs
 // cost next to nothing and the kernel only streams W*, one persistent CTA per SM with a deep ring. An epilogue thread owns
