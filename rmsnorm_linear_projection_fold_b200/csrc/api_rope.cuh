@@ -67,14 +67,13 @@ fn_status flashnorm_rope(const void* x, const void* rope_cs, const void* positio
   int dev = 0;
   const int sms = device_sm_count(&dev);
   if (sms <= 0) return fail(FN_ERR_CUDA, "cannot query the current device");
-  const int vec = static_cast<int>(16 / es);
-  // 16-byte accesses need aligned bases and strides and whole units; everything else goes feature by feature
+  // the widest access that bases, strides and sizes allow: 16 bytes, or less for heads like 38 or 210 features
   const bool half = layout == FN_ROPE_HALF;
-  const bool wide = aligned16(x) && aligned16(y) && head_dim % vec == 0 && x_row_stride % vec == 0 &&
-                    x_head_stride % vec == 0 && y_row_stride % vec == 0 && y_head_stride % vec == 0 &&
-                    (!half || (rot_dim / 2) % vec == 0);
-  const int64_t v = wide ? vec : 1;
-  const int64_t units = half || !wide ? rot_dim / 2 / v + (head_dim - rot_dim) / v : head_dim / v;
+  int v = static_cast<int>(16 / es);
+  while (v > 1 && ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y)) % (v * es) != 0 ||
+                   (head_dim | x_row_stride | x_head_stride | y_row_stride | y_head_stride | (half ? rot_dim / 2 : 0)) % v != 0))
+    v /= 2;
+  const int64_t units = half || v == 1 ? rot_dim / 2 / v + (head_dim - rot_dim) / v : head_dim / v;
   fn::RopeParams p;
   p.x = x;
   p.y = y;
@@ -90,11 +89,18 @@ fn_status flashnorm_rope(const void* x, const void* rope_cs, const void* positio
   p.sign = backward ? -1.0f : 1.0f;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == FN_BF16) {
-    if (wide) return half ? launch_rope<uint16_t, 8, true>(p, s) : launch_rope<uint16_t, 8, false>(p, s);
-    return half ? launch_rope<uint16_t, 1, true>(p, s) : launch_rope<uint16_t, 1, false>(p, s);
+    switch (v) {
+      case 8: return half ? launch_rope<uint16_t, 8, true>(p, s) : launch_rope<uint16_t, 8, false>(p, s);
+      case 4: return half ? launch_rope<uint16_t, 4, true>(p, s) : launch_rope<uint16_t, 4, false>(p, s);
+      case 2: return half ? launch_rope<uint16_t, 2, true>(p, s) : launch_rope<uint16_t, 2, false>(p, s);
+      default: return half ? launch_rope<uint16_t, 1, true>(p, s) : launch_rope<uint16_t, 1, false>(p, s);
+    }
   }
-  if (wide) return half ? launch_rope<float, 4, true>(p, s) : launch_rope<float, 4, false>(p, s);
-  return half ? launch_rope<float, 1, true>(p, s) : launch_rope<float, 1, false>(p, s);
+  switch (v) {
+    case 4: return half ? launch_rope<float, 4, true>(p, s) : launch_rope<float, 4, false>(p, s);
+    case 2: return half ? launch_rope<float, 2, true>(p, s) : launch_rope<float, 2, false>(p, s);
+    default: return half ? launch_rope<float, 1, true>(p, s) : launch_rope<float, 1, false>(p, s);
+  }
 }
 
 fn_status flashnorm_rope_table_scaled(void* rope_cs, int64_t max_pos, int64_t rot_dim, double base, int scaling,

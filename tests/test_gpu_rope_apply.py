@@ -56,7 +56,8 @@ def _check(y, x, cs, pos, n_rope, layout, backward):
     (3, 5, 64, 64, 3, 0),      # whole heads, two of them carried over
     (17, 4, 128, 32, 4, 2),    # a part of the head, heads inside wider rows
     (5, 3, 80, 20, 2, 0),      # rot/2 no multiple of a 16-byte access
-    (9, 2, 38, 34, 2, 1),      # head_dim and strides that no wide access fits; a unit straddling rot_dim
+    (9, 2, 38, 34, 2, 1),      # head_dim and strides that only narrow accesses fit; rot/2 odd
+    (11, 3, 44, 24, 3, 0), (11, 3, 44, 26, 2, 1), (4, 2, 46, 12, 2, 1), (6, 7, 210, 210, 5, 0),  # accesses of 4, 2 and 1 features
     (33, 2, 72, 36, 1, 0),     # rot_dim ends inside a wide access (interleaved)
     (700, 40, 128, 128, 33, 0),  # several heads per thread, the last set ragged
     (4, 2, 16, 16, 0, 0),      # nothing turned
