@@ -347,12 +347,15 @@ FN_API fn_status flashnorm_int8_workspace_bytes(int64_t M, int64_t d, int64_t N,
  *   gain multiplied in: V itself needs no alignment), targets int64 [M] ->
  *   loss and lse, fp32 [M]. A row whose target is ignore_index has loss 0 (its lse is computed all the same). A target
  *   that is neither a class (0 .. V-1) nor ignore_index gives that row a NaN loss, and the next
- *   flashnorm_check_device_error returns FN_ERR_INVALID_ARG.
+ *   flashnorm_check_device_error returns FN_ERR_INVALID_ARG. The target's logit is a dot product of its own in fp32, here
+ *   and in the gradient, with the same bits: what is left of a row that is predicted well does not depend on how the tensor
+ *   cores add. Other logits of one-signed products are up to 2.4e-6 (relative) low.
  * flashnorm_linear_cross_entropy_backward: g fp32 [M] (dL/dloss), x, Wstar, targets as above and the forward's lse ->
  *   dx bf16 [M, d] and dWstar bf16 [V, d], both overwritten. With dl[m][n] = g[m] (exp(l[m][n] - lse[m]) - [n = t[m]]):
  *     dW*[n] = sum_m r[m] dl[m][n] x[m],   dx[m] = r[m] sum_n dl[m][n] W*[n] - x[m] (r[m]^2 / d) sum_n dl[m][n] l[m][n]
  *   Rows whose target is ignore_index have a zero dx and take no part in dW*; a bad target gives its row a NaN dx, takes
- *   no part in dW* and is reported as above. r dl is rounded to bf16 once for the two products, but for the
+ *   no part in dW* and is reported as above. lse is fp32, so the target's dl is known to 3.5e-6 g (|l| < 32): 0.35 % of
+ *   itself where the target's probability is 0.999. r dl is rounded to bf16 once for the two products, but for the
  *   target's own entry, which stays fp32 (for dW* not where a class is frequent); sums are fp32. M == 0
  *   sets dWstar to zero.
  * flashnorm_cross_entropy_workspace_bytes: the scratch a call (backward: 0 or 1) of this shape needs on the current

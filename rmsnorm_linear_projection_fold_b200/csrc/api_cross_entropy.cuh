@@ -56,7 +56,7 @@ struct CePlan {
   int ksplit;      // K ranges of dx's product, and of dW*'s where it goes through planes
   int dw_ksplit;
   int64_t arrived, rstd, part, tlogit;               // forward
-  int64_t n_live, rows, rank_of, target, u, hits, xc, P, acc, dw_acc, bytes;  // backward (and part)
+  int64_t n_live, rows, rank_of, target, u, ct, hits, xc, P, acc, dw_acc, bytes;  // backward (and part)
 };
 
 // Stages per accumulation of the forward's logits: 1024 k. At k = 4096 the loss is then 3.4e-7 off (relative), 1.5e-6 with one
@@ -122,8 +122,7 @@ CePlan ce_plan(int64_t M, int64_t d, int64_t V, bool backward, int sms) {
       c.bytes = c.tlogit + round_up(4 * M, 256);
       return c;
     }
-    c.tlogit = c.part + round_up(8ll * kCeFwdParts * c.n_tiles * M, 256);
-    c.bytes = c.tlogit + round_up(4 * M, 256);
+    c.bytes = c.part + round_up(8ll * kCeFwdParts * c.n_tiles * M, 256);
     return c;
   }
   fn::PairGemmParams w;
@@ -137,7 +136,8 @@ CePlan ce_plan(int64_t M, int64_t d, int64_t V, bool backward, int sms) {
   c.rank_of = c.rows + round_up(16 * M, 256);
   c.target = c.rank_of + round_up(4 * M, 256);
   c.u = c.target + round_up(4 * M, 256);
-  c.hits = c.u + round_up(4 * M, 256);
+  c.ct = c.u + round_up(4 * M, 256);
+  c.hits = c.ct + round_up(4 * M, 256);
   c.part = c.hits + round_up(4 * ((c.piece + 31) / 32) * ce_ld_hits(M), 256);
   c.xc = c.part + round_up(4ll * fn::CeGradEpi::kParts * c.n_tiles * c.pieces * M, 256);
   c.P = c.xc + round_up(2 * Mp * d, 256);
@@ -232,7 +232,10 @@ fn_status flashnorm_linear_cross_entropy(const void* x, const void* Wstar, const
     p.arrived = reinterpret_cast<unsigned*>(base + c.arrived);
     p.loss = static_cast<float*>(loss);
     p.lse = static_cast<float*>(lse);
+    p.x = static_cast<const uint16_t*>(x);
+    p.W = static_cast<const uint16_t*>(Wstar);
     p.M = static_cast<int>(M);
+    p.K = static_cast<int>(d);
     p.V = static_cast<int>(V);
     p.num_kb = static_cast<int>((d + 63) / 64);
     p.ignore = ignore_index;
@@ -247,7 +250,6 @@ fn_status flashnorm_linear_cross_entropy(const void* x, const void* Wstar, const
   ep.rstd = rstd;
   ep.targets = static_cast<const long long*>(targets);
   ep.part = reinterpret_cast<float2*>(base + c.part);
-  ep.tlogit = reinterpret_cast<float*>(base + c.tlogit);
   fn::PairGemmParams p;
   plan_pair_gemm(&p, M, V, (d + 63) / 64, sms, 32);
   p.kchunk = kCeFwdChunk;
@@ -262,8 +264,9 @@ fn_status flashnorm_linear_cross_entropy(const void* x, const void* Wstar, const
            : launch_pair_gemm<fn::PG_BF16, fn::PgJob<false, false, fn::CeFwdEpi<false>>>(tx, tw, p, ep, sms, dev, s, what);
   if (st != FN_OK) return st;
   cudaError_t e = launch_kernel(fn::k_ce_join, dim3(static_cast<unsigned>((M + 7) / 8)), dim3(256), 0, s, 1,
-                                static_cast<const float2*>(ep.part), static_cast<const float*>(ep.tlogit), ep.targets,
-                                static_cast<float*>(loss), static_cast<float*>(lse), p.M, p.N, kCeFwdParts * p.num_n_tiles,
+                                static_cast<const float2*>(ep.part), ep.rstd, static_cast<const uint16_t*>(x),
+                                static_cast<const uint16_t*>(Wstar), ep.targets, static_cast<float*>(loss),
+                                static_cast<float*>(lse), p.M, static_cast<int>(d), p.N, kCeFwdParts * p.num_n_tiles,
                                 static_cast<long long>(ignore_index));
   return e == cudaSuccess ? FN_OK : cuda_fail(e, "cross entropy join launch");
 }
@@ -297,6 +300,7 @@ fn_status flashnorm_linear_cross_entropy_backward(const void* g, const void* x, 
   uint16_t* xc = reinterpret_cast<uint16_t*>(base + c.xc);
   const fn::CeLive live = {n_live, reinterpret_cast<int*>(base + c.target), reinterpret_cast<float*>(base + c.u),
                           reinterpret_cast<unsigned*>(base + c.hits), static_cast<int>(ce_ld_hits(M))};
+  float* ct = reinterpret_cast<float*>(base + c.ct);
   float* cpart = reinterpret_cast<float*>(base + c.part);
   uint16_t* P = reinterpret_cast<uint16_t*>(base + c.P);
   float* acc = reinterpret_cast<float*>(base + c.acc);
@@ -305,7 +309,8 @@ fn_status flashnorm_linear_cross_entropy_backward(const void* g, const void* x, 
   const int64_t per_block = round_up((M + 255) / 256, 8);
   cudaError_t e = launch_kernel(fn::k_ce_pack, dim3(static_cast<unsigned>((M + per_block - 1) / per_block)), dim3(256), 0, s, 1,
                                 static_cast<const uint16_t*>(x), static_cast<const long long*>(targets),
-                                static_cast<const float*>(lse), static_cast<const float*>(g), xc, rows, live.target, rank_of, n_live,
+                                static_cast<const float*>(lse), static_cast<const float*>(g),
+                                static_cast<const uint16_t*>(Wstar), xc, rows, live.target, live.u, ct, rank_of, n_live,
                                 static_cast<int>(M), static_cast<int>(d), static_cast<int>(V),
                                 static_cast<int>(per_block), eps, static_cast<long long>(ignore_index));
   if (e != cudaSuccess) return cuda_fail(e, "cross entropy pack launch");
@@ -362,7 +367,7 @@ fn_status flashnorm_linear_cross_entropy_backward(const void* g, const void* x, 
   const bool narrow = d / 8 * c.ksplit + parts <= 128;  // loads of a row: a warp for it, else a block
   e = launch_kernel(narrow ? fn::k_ce_dx<32> : fn::k_ce_dx<256>, dim3(static_cast<unsigned>(narrow ? (M + 7) / 8 : M)), dim3(256), 0, s,
                     1, static_cast<const float*>(acc), static_cast<const float*>(cpart), static_cast<const fn::CeRow*>(rows),
-                    static_cast<const float*>(live.u), static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(Wstar),
+                    static_cast<const float*>(live.u), static_cast<const float*>(ct), static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(Wstar),
                     static_cast<const int*>(rank_of), static_cast<uint16_t*>(dx), static_cast<int>(M), static_cast<int>(d),
                     c.ksplit, parts);
   return e == cudaSuccess ? FN_OK : cuda_fail(e, "cross entropy dx launch");

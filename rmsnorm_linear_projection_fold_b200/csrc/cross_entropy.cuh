@@ -7,11 +7,17 @@
 // Forward (more than 32 rows; fewer: cross_entropy_small.cuh): the logits of a 256-row tile exist only in tensor memory;
 // each epilogue thread owns a row and keeps the running maximum and sum of exponentials of its columns, one (max, sum)
 // pair per row, column tile and warp goes to the workspace, and a second kernel joins them in a fixed order.
+// The target's logit is a dot product of its own, in fp32 by one warp (ce_row_dot: x and W*'s row once more, 2 d elements a
+// row), and takes the place of the tensor core's in lse, in the loss and in the gradient. Where the model predicts a row well
+// the loss and the target's entry of dl are what is left of exp(l - lse) near 1, and the tensor core's sum is not good enough
+// for that: products of one sign are all cut the same way (l = 16.7, d = 4096, sums of 1024 k: 4e-5 low; over all k 1.5e-4),
+// so that at 1 - p = 1e-3 the target's row of dW* was 24 % off (0.4 % now). In the join the dot product hides behind
+// the product's last tiles.
 // Backward: rows without a target have no gradient, so the live rows are packed first and only they go through the three
 // products (a batch half of prompt or padding costs half; what such rows hold cannot reach dW*). Then, in pieces of the
 // vocabulary, the logits are computed again and leave the chip as the factor both gradients share,
 //     P[m, n] = r[m] dl[m, n] in bf16,   dl[m, n] = g[m] (exp(l - lse) - [n = t]),
-// except for the target's own entry u[m] = r dl[m, t], which stays fp32 (P is 0 there; in blocks of 32 rows where three
+// except for the target's own entry u[m] = r dl[m, t], which is taken from ce_row_dot and stays fp32 (P is 0 there; in blocks of 32 rows where three
 // targets or more lie within 32 classes of a large vocabulary P has it rounded, and u is the rest, which dW* then leaves out):
 //     dW*[n, :] = sum_m P[m, n] x[m, :] + sum_{m: t[m] = n} u[m] x[m, :]
 //     dx[m, :]  = sum_n P[m, n] W*[n, :] + u[m] W*[t, :] - x[m, :] (r[m]^2 / d) c[m],   c[m] = sum_n dl[m, n] l[m, n]
@@ -69,13 +75,38 @@ __global__ void __launch_bounds__(256) k_row_rstd(const uint16_t* __restrict__ x
 // What a target says: a class, nothing (ignore_index), or neither (reported to the host).
 __device__ __forceinline__ bool target_is_class(long long t, int V) { return t >= 0 && t < V; }
 
+// x . w of two bf16 rows by a warp in fp32, eight sums a lane, rounded to nearest: within about 2^-24 sqrt(d) of the products'
+// magnitudes. The same bits wherever it is taken (lane l adds pieces l, l + 32, ... in order), so that the forward's lse and
+// the gradient's logit of a target cancel.
+struct CeDot {
+  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  __device__ __forceinline__ void add(const uint4& a, const uint4& b) {
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      s[2 * e] = fmaf(bf16lo_to_f32(u[e]), bf16lo_to_f32(v[e]), s[2 * e]);
+      s[2 * e + 1] = fmaf(bf16hi_to_f32(u[e]), bf16hi_to_f32(v[e]), s[2 * e + 1]);
+    }
+  }
+  __device__ __forceinline__ float total() const {
+    return warp_sum(((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7])));
+  }
+};
+__device__ __forceinline__ float ce_row_dot(const uint16_t* x, const uint16_t* w, int K, int lane) {
+  const uint4* a = reinterpret_cast<const uint4*>(x);
+  const uint4* b = reinterpret_cast<const uint4*>(w);
+  CeDot dot;
+#pragma unroll 4
+  for (int c = lane; c < (K >> 3); c += 32) dot.add(__ldcg(a + c), __ldcg(b + c));
+  return dot.total();
+}
+
 // ---------------------------------------------------------------------------------------------- forward
 
 struct CeFwdParams {
   const float* rstd;
   const long long* targets;
-  float2* part;   // [M][kParts column tiles]: running maximum (of log2 e times the logits) and sum of 2^(. - max)
-  float* tlogit;  // [M] logit of the target
+  float2* part;  // [M][kParts column tiles]: running maximum (of log2 e times the logits) and sum of 2^(. - max), the target left out
 };
 
 // A thread's columns of a tile are up to kChunks chunks of 32, shared out among the quarter's warps. HELD: the tile takes
@@ -85,13 +116,12 @@ struct CeFwdEpi {
   static constexpr int kParts = 4;
   static constexpr int kChunks = 8 / kParts;
   using Params = CeFwdParams;
-  float rstd, r2;  // r2 = r log2(e): the exponentials are powers of two
+  float r2;  // r log2(e): the exponentials are powers of two
   long long tgt;
   float held[HELD ? kChunks : 1][32];
   __device__ __forceinline__ CeFwdEpi(const Params& e, const PairGemmParams& p, const PgTile& t, int lane) {
     const int row = t.row0 + lane;
-    rstd = row < t.M ? __ldcg(e.rstd + row) : 0.f;
-    r2 = rstd * kLog2e;
+    r2 = row < t.M ? __ldcg(e.rstd + row) * kLog2e : 0.f;
     tgt = row < t.M ? __ldg(e.targets + row) : -1;
     if (HELD) {
 #pragma unroll
@@ -137,19 +167,17 @@ struct CeFwdEpi {
         for (int j = 0; j < kCols; ++j)
           z[j] = (HELD ? held[HELD ? i * kCols / 32 : 0][HELD ? i * kCols % 32 + j : 0] : 0.f) + __uint_as_float(v[j >> 4][j & 15]);
       }
-      const long long at = tgt - (t.n0 + c0);
-      if (at >= 0 && at < kCols) {
-        float lt = 0.f;
-#pragma unroll
-        for (int j = 0; j < kCols; ++j)
-          if (at == j) lt = z[j];
-        if (c0 + at < t.width) e.tlogit[row] = lt * rstd;
-      }
       const bool edge = c0 + kCols > t.width;  // columns past the vocabulary take no part
       if (edge) {
 #pragma unroll
         for (int j = 1; j < kCols; ++j)
           if (c0 + j >= t.width) z[j] = z[0];
+      }
+      const long long at = tgt - (t.n0 + c0);
+      if (at >= 0 && at < kCols) {  // the target joins the row at the end
+#pragma unroll
+        for (int j = 0; j < kCols; ++j)
+          if (at == j) z[j] = -INFINITY;
       }
       float mc = z[0];
 #pragma unroll
@@ -182,14 +210,12 @@ struct CeFwdEpi {
 };
 
 // lse and loss of a row by LANES consecutive lanes: each joins every LANES-th partial pair, then they join in a butterfly (a
-// fixed order). BATCH pairs of a lane are loaded at once. An ignored row's loss is 0; a target that is neither a class nor
-// ignore_index gives NaN and is reported. Every lane of the warp calls, live or not.
+// fixed order), and last the target's logit, rstd zt. BATCH pairs of a lane are loaded at once. An ignored row's loss is 0;
+// a target t that is neither a class nor ignore_index gives NaN and is reported. Every lane of the warp calls, live or not.
 template <int LANES, int BATCH>
-__device__ __forceinline__ void ce_join_row(const float2* part, int parts, const float* tlogit, const long long* targets,
-                                            float* loss, float* lse, int row, bool live, int V, long long ignore, int lane) {
+__device__ __forceinline__ void ce_join_row(const float2* part, int parts, float rstd, float zt, long long t, float* loss,
+                                            float* lse, int row, bool live, int V, long long ignore, int lane) {
   const int sub = lane % LANES;
-  const long long t = live ? targets[row] : ignore;
-  const float lt = live ? __ldcg(tlogit + row) : 0.f;  // not written, nor used, where t is no class
   const float2* src = part + static_cast<size_t>(live ? row : 0) * parts;
   float m = -INFINITY, s = 0.f;
   auto join = [&](float qm, float qs) {
@@ -216,12 +242,14 @@ __device__ __forceinline__ void ce_join_row(const float2* part, int parts, const
 #pragma unroll
   for (int o = LANES / 2; o > 0; o >>= 1) join(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
   if (sub == 0 && live) {
-    const float z = m * kLn2 + logf(s);
-    lse[row] = z;
+    const float lt = zt * (rstd * kLog2e);
+    if (target_is_class(t, V)) join(lt, 1.0f);
+    const float ls = logf(s);
+    lse[row] = m * kLn2 + ls;
     if (t == ignore) {
       loss[row] = 0.f;
     } else if (target_is_class(t, V)) {
-      loss[row] = z - lt;
+      loss[row] = fmaf(m - lt, kLn2, ls);  // lse - l_t, without the rounding of lse
     } else {
       loss[row] = __int_as_float(0x7fc00000);
       atomicOr(&g_device_status, kStatusBadTarget);
@@ -229,13 +257,19 @@ __device__ __forceinline__ void ce_join_row(const float2* part, int parts, const
   }
 }
 
-__global__ void __launch_bounds__(256) k_ce_join(const float2* __restrict__ part, const float* __restrict__ tlogit,
+// A warp per row. x, W* and the targets are in place before the product starts (the row statistics' pass waited for them), so
+// the target's logit is taken before the wait.
+__global__ void __launch_bounds__(256) k_ce_join(const float2* __restrict__ part, const float* __restrict__ rstd,
+                                                 const uint16_t* __restrict__ x, const uint16_t* __restrict__ W,
                                                  const long long* __restrict__ targets, float* __restrict__ loss,
-                                                 float* __restrict__ lse, int M, int V, int parts, long long ignore) {
+                                                 float* __restrict__ lse, int M, int K, int V, int parts, long long ignore) {
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const long long t = row < M ? __ldcg(targets + row) : ignore;
+  const float zt = row < M && target_is_class(t, V)
+                       ? ce_row_dot(x + static_cast<size_t>(row) * K, W + static_cast<size_t>(t) * K, K, lane) : 0.f;
   grid_dep_wait();
   grid_dep_launch();
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  ce_join_row<32, 10>(part, parts, tlogit, targets, loss, lse, row, row < M, V, ignore, lane);
+  ce_join_row<32, 10>(part, parts, row < M ? __ldcg(rstd + row) : 0.f, zt, t, loss, lse, row, row < M, V, ignore, lane);
 }
 
 // ---------------------------------------------------------------------------------------------- backward
@@ -250,7 +284,7 @@ struct __align__(16) CeRow {
 struct CeLive {
   const int* n_live;
   int* target;  // [live rows]
-  float* u;     // r dl of the target's entry, less what P has of it
+  float* u;     // r dl of the target's entry, from where P has it less that
   // [32 vocabulary columns of the piece][ld_hits: 32 live rows]: which of these rows have their target among these columns
   // and its entry not in P
   unsigned* hits;
@@ -259,13 +293,15 @@ struct CeLive {
 
 constexpr int kCeIgnored = -1, kCeBad = -2;  // in place of a row's rank among the live ones
 
-// Packs the live rows in order: xc[rank] = x[m], rows[rank], rank_of[m], and their number. Rows up to the next multiple of
+// Packs the live rows in order: xc[rank] = x[m], rows[rank], the target's entry u[rank] and its share ct[rank] of c / r,
+// rank_of[m], and their number. Rows up to the next multiple of
 // 64 are zeroed: dW*'s product runs over whole stages of 64 rows. A block serves rows_per_block rows, a warp an eighth of
 // them in order; each counts the live rows before its own, from the targets.
-__global__ void __launch_bounds__(256) k_ce_pack(const uint16_t* __restrict__ x, const long long* __restrict__ targets,
+__global__ void __launch_bounds__(256, 2) k_ce_pack(const uint16_t* __restrict__ x, const long long* __restrict__ targets,
                                                  const float* __restrict__ lse, const float* __restrict__ g,
-                                                 uint16_t* __restrict__ xc, CeRow* __restrict__ rows,
-                                                 int* __restrict__ target, int* __restrict__ rank_of,
+                                                 const uint16_t* __restrict__ W, uint16_t* __restrict__ xc,
+                                                 CeRow* __restrict__ rows, int* __restrict__ target, float* __restrict__ u,
+                                                 float* __restrict__ ct, int* __restrict__ rank_of,
                                                  int* __restrict__ n_live, int M, int K, int V,
                                                  int rows_per_block, float eps, long long ignore) {
   grid_dep_wait();
@@ -279,16 +315,25 @@ __global__ void __launch_bounds__(256) k_ce_pack(const uint16_t* __restrict__ x,
   const int b0 = static_cast<int>(blockIdx.x) * rows_per_block;
   const int per_warp = rows_per_block >> 3, m0 = b0 + warp * per_warp;
   const int chunks = K >> 3;
-  // a row's first kHeld * 256 elements go through registers; those of the warp's first row are loaded ahead of the count
+  // a row's first kHeld * 256 elements go through registers, and the first 4 * 256 of its target's row of W*; those of the
+  // warp's first row are loaded ahead of the count
   constexpr int kHeld = 16;
-  uint4 held[kHeld];
-  auto load_row = [&](int m) {
+  uint4 held[kHeld], w[4];
+  auto load_w = [&](long long t, int i0) {
+    const uint4* wt = reinterpret_cast<const uint4*>(W + static_cast<size_t>(t) * K);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = lane + 32 * (i0 + i) < chunks ? __ldcg(wt + lane + 32 * (i0 + i)) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  auto load_row = [&](int m, long long t) {
     const uint4* src = reinterpret_cast<const uint4*>(x + static_cast<size_t>(m) * K);
 #pragma unroll
     for (int i = 0; i < kHeld; ++i)
       held[i] = lane + 32 * i < chunks ? __ldcg(src + lane + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+    if (target_is_class(t, V)) load_w(t, 0);
   };
-  if (m0 < M) load_row(m0);
+  long long t = m0 < M ? __ldg(targets + m0) : ignore;
+  if (m0 < M) load_row(m0, t);
   int n = 0;
 #pragma unroll 8
   for (int m = threadIdx.x; m < b0; m += 256) n += live_at(m);
@@ -304,14 +349,17 @@ __global__ void __launch_bounds__(256) k_ce_pack(const uint16_t* __restrict__ x,
     return __reduce_add_sync(0xffffffffu, c);
   };
   int rank = base + count(b0, min(m0, M));
-  for (int m = m0; m < min(m0 + per_warp, M); ++m) {
-    const long long t = __ldg(targets + m);
+  long long t_next;
+  for (int m = m0; m < min(m0 + per_warp, M); ++m, t = t_next) {
+    t_next = m + 1 < M ? __ldg(targets + m + 1) : ignore;
     const bool live = t != ignore && target_is_class(t, V);
     if (lane == 0) rank_of[m] = live ? rank : t == ignore ? kCeIgnored : kCeBad;
     if (!live) continue;
     const uint4* src = reinterpret_cast<const uint4*>(x + static_cast<size_t>(m) * K);
+    const uint4* wt = reinterpret_cast<const uint4*>(W + static_cast<size_t>(t) * K);
     uint4* dst = reinterpret_cast<uint4*>(xc + static_cast<size_t>(rank) * K);
     float s0 = 0.f, s1 = 0.f;
+    CeDot dot;
     auto take = [&](const uint4& v) {
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -321,19 +369,26 @@ __global__ void __launch_bounds__(256) k_ce_pack(const uint16_t* __restrict__ x,
         s1 = fmaf(b, b, s1);
       }
     };
-    if (m != m0) load_row(m);
+    if (m != m0) load_row(m, t);
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      if (lane + 32 * i < chunks) dst[lane + 32 * i] = held[i];
-      take(held[i]);
+    for (int i0 = 0; i0 < kHeld; i0 += 4) {
+      if (i0 > 0) load_w(t, i0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4& v = held[i0 + i];
+        if (lane + 32 * (i0 + i) < chunks) dst[lane + 32 * (i0 + i)] = v;
+        take(v);
+        dot.add(v, w[i]);
+      }
     }
-#pragma unroll 4
+#pragma unroll 2
     for (int c = lane + 32 * kHeld; c < chunks; c += 32) {
-      const uint4 v = __ldcg(src + c);
+      const uint4 v = __ldcg(src + c), w = __ldcg(wt + c);
       dst[c] = v;
       take(v);
+      dot.add(v, w);
     }
-    const float ss = warp_sum(s0 + s1);
+    const float ss = warp_sum(s0 + s1), zt = dot.total();
     if (lane == 0) {
       CeRow r;
       r.rstd = 1.0f / sqrtf(ss / static_cast<float>(K) + eps);
@@ -342,6 +397,9 @@ __global__ void __launch_bounds__(256) k_ce_pack(const uint16_t* __restrict__ x,
       r.target = static_cast<int>(t);
       rows[rank] = r;
       target[rank] = r.target;
+      const float ut = r.g * r.rstd * (ex2(fmaf(zt, r.rstd * kLog2e, r.nlse2)) - 1.0f);
+      u[rank] = ut;
+      ct[rank] = ut * zt;
     }
     ++rank;
   }
@@ -359,7 +417,7 @@ __global__ void __launch_bounds__(256) k_ce_pack(const uint16_t* __restrict__ x,
 struct CeGradParams {
   const CeRow* rows;
   uint16_t* P;     // bf16 [live rows, and up to the next multiple of 64][ldp], this piece's columns
-  float* cpart;    // [kParts column tiles][M] partial c, this piece's
+  float* cpart;    // [kParts column tiles][M] partial c without the targets' share, this piece's
   int ldp;         // a multiple of 64: rows of P start on whole 128-byte lines
   int v0;          // first column of the piece within the vocabulary
   int often;       // targets in a block of 32 rows and 32 classes from which on P has them
@@ -385,7 +443,7 @@ struct CeGradEpi {
     const float r2 = q.rstd * kLog2e, gr = q.g * q.rstd;
     const uint64_t rr = pack_f32x2(r2, r2), nl = pack_f32x2(q.nlse2, q.nlse2), gg = pack_f32x2(gr, gr);
     uint64_t c2 = 0;  // sum of exp(l - lse) z; c = g r times it
-    float ct = 0.f;   // the target's -z
+    float ct = 0.f;   // the target's share of that, negative: c takes it from ce_row_dot
     const int t0 = q.target - (e.v0 + t.n0);  // the target's column in this tile, if it has it
     for (int ch = t.part; ch * 32 < t.width; ch += kParts) {
       const int c0 = ch * 32;
@@ -427,14 +485,16 @@ struct CeGradEpi {
       const bool often = __popc(hits) >= e.often;
       if (lane == 0) e.live.hits[static_cast<size_t>((t.n0 + c0) >> 5) * e.live.ld_hits + (t.row0 >> 5)] = often ? 0u : hits;
       if (hit) {  // the target's entry: kept in fp32, 0 in P, or what its rounding in P leaves of it
-        float z = 0.f;
+        float z = 0.f, in_p = 0.f;
 #pragma unroll
         for (int j = 0; j < 32; ++j)
           if (at == j) z = __uint_as_float(v[j >> 4][j & 15]);
-        const float u = gr * (ex2(fmaf(z, r2, q.nlse2)) - 1.0f);
-        const float in_p = often ? bf16lo_to_f32(pack_bf16x2(u, 0.f) & 0xFFFFu) : 0.f;
-        e.live.u[row] = u - in_p;
-        ct = -z;
+        ct = -z * ex2(fmaf(z, r2, q.nlse2));
+        if (often) {
+          const float u = __ldcg(e.live.u + row);
+          in_p = bf16lo_to_f32(pack_bf16x2(u, 0.f) & 0xFFFFu);
+          e.live.u[row] = u - in_p;
+        }
 #pragma unroll
         for (int j = 0; j < 32; ++j)
           if (at == j) {
@@ -736,6 +796,7 @@ __global__ void __launch_bounds__(256) k_ce_dw(const float* __restrict__ acc, co
 template <int LPR>
 __global__ void __launch_bounds__(256) k_ce_dx(const float* __restrict__ acc, const float* __restrict__ cpart,
                                                const CeRow* __restrict__ rows, const float* __restrict__ u,
+                                               const float* __restrict__ ct,
                                                const uint16_t* __restrict__ x, const uint16_t* __restrict__ W,
                                                const int* __restrict__ rank_of, uint16_t* __restrict__ dx, int M, int K,
                                                int planes, int parts) {
@@ -754,7 +815,7 @@ __global__ void __launch_bounds__(256) k_ce_dx(const float* __restrict__ acc, co
     return;
   }
   const float4 meta = __ldcg(reinterpret_cast<const float4*>(rows + rank));
-  const float r = meta.x, ut = __ldcg(u + rank);
+  const float r = meta.x, ut = __ldcg(u + rank), c_t = __ldcg(ct + rank);
   const uint4* wr = reinterpret_cast<const uint4*>(W + static_cast<size_t>(__float_as_int(meta.w)) * K);
   const uint4* xr = reinterpret_cast<const uint4*>(x + static_cast<size_t>(row) * K);
   const float4* ar = reinterpret_cast<const float4*>(acc + static_cast<size_t>(rank) * K);
@@ -781,7 +842,7 @@ __global__ void __launch_bounds__(256) k_ce_dx(const float* __restrict__ acc, co
     __syncthreads();
     c = ((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7]));
   }
-  const float k = r * r / static_cast<float>(K) * c;
+  const float k = r * r / static_cast<float>(K) * (c + c_t);
   for (int i0 = sub; i0 < chunks; i0 += kAhead * LPR) {
     if (i0 != sub) load(i0);
 #pragma unroll

@@ -7,7 +7,8 @@
 // per token, and the last CTA to arrive joins all of them in a fixed order. The pass before it takes 1/rms and zeroes the
 // arrival counter; W* and x do not depend on it and are fetched meanwhile, so it reads nothing but x: its loads queue behind
 // W*'s, and when it fetched the targets' rows of W* for their logits too, the epilogue waited for it (23 rows x 576 x
-// 49152, call after call: 18.4 us, 17.7 so). A target's logit is taken by the thread whose row it is.
+// 49152, call after call: 18.4 us, 17.7 so). The targets' logits (ce_row_dot) are taken by the epilogue warps before they wait
+// for that pass, a row per CTA where there are enough CTAs.
 //
 // Bound: HBM. 23 x 576 x 49152: 16.8 us for 57 MB (8.7 at the copy rate): 4 to start, 3 a slab, 2.5 for the join (a warp per
 // token instead of 8 lanes: 6.4). The CTA-pair product, which spends 256 rows of MMA on them, takes 19.5 and a join of 5.
@@ -32,13 +33,15 @@ __host__ __device__ constexpr int ce_small_smem_bytes(int tokens) {
 
 struct CeSmallParams {
   const float* rstd;
-  float* tlogit;      // [M]
+  float* tlogit;      // [M] x . W*[target]
+  const uint16_t* x;
+  const uint16_t* W;
   const long long* targets;
   float2* part;       // [M][CTAs]
   unsigned* arrived;  // zeroed by the pass before
   float* loss;
   float* lse;
-  int M, V, num_kb;
+  int M, K, V, num_kb;
   long long ignore;
 };
 
@@ -187,6 +190,12 @@ __global__ void __launch_bounds__(kCsThreads, 1)
   } else {
     // ------------------------------------------------------------------ epilogue
     const int w = warp - 2, q = warp & 3, half = w >> 2;
+    for (int row = static_cast<int>(blockIdx.x) + w * static_cast<int>(gridDim.x); row < p.M; row += 8 * static_cast<int>(gridDim.x)) {
+      const long long t = __ldcg(p.targets + row);
+      if (!target_is_class(t, p.V)) continue;
+      const float zt = ce_row_dot(p.x + static_cast<size_t>(row) * p.K, p.W + static_cast<size_t>(t) * p.K, p.K, lane);
+      if (lane == 0) p.tlogit[row] = zt;
+    }
     grid_dep_wait();
     // lane j: the target of the warp's token j
     const long long target = lane < NT && half * NT + lane < p.M ? __ldg(p.targets + half * NT + lane) : -1;
@@ -226,18 +235,15 @@ __global__ void __launch_bounds__(kCsThreads, 1)
         if (acc == 0) acc_ph ^= 1u;
       }
       const long long row = target - (static_cast<long long>(slab) * kCsRows + q * 32);
+      unsigned mine = 0;  // tokens whose target is this row: their logits join at the end
       for (unsigned hits = __ballot_sync(0xffffffffu, ok && row >= 0 && row < 32); hits != 0; hits &= hits - 1) {
         const int j0 = __ffs(hits) - 1;
-        if (__shfl_sync(0xffffffffu, static_cast<int>(row), j0) != lane) continue;
-        float v = 0.f;
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-          if (j == j0) v = z[j];
-        p.tlogit[half * NT + j0] = v * __ldcg(p.rstd + half * NT + j0);
+        if (__shfl_sync(0xffffffffu, static_cast<int>(row), j0) == lane) mine |= 1u << j0;
       }
       if (ok && slab * kCsRows + q * 32 + lane < p.V) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
+          if (mine >> j & 1u) continue;
           const float d = fmaf(z[j], r2[j], -m[j]);
           const float e = ex2(-fabsf(d));
           s[j] = d > 0.f ? fmaf(s[j], e, 1.0f) : s[j] + e;
@@ -280,9 +286,15 @@ __global__ void __launch_bounds__(kCsThreads, 1)
     named_bar_sync(1, 256);  // the CTA's pairs come before its arrival (barrier, then release)
     if (threadIdx.x == 64) *arrival = atom_add_acq_rel_gpu(p.arrived, 1u);
     named_bar_sync(1, 256);
-    if (*arrival == gridDim.x - 1)
+    if (*arrival == gridDim.x - 1) {
+      const int row = tok / kJoin;
+      const bool live = row < p.M;
+      // the logit is not written, nor used, where the target is no class
+      const float zt = live ? __ldcg(p.tlogit + row) : 0.f, rstd = live ? __ldcg(p.rstd + row) : 0.f;
+      const long long t = live ? __ldcg(p.targets + row) : p.ignore;
       // all tokens at once, 19 pairs of each lane in flight: every other SM is idle meanwhile
-      ce_join_row<kJoin, 19>(p.part, parts, p.tlogit, p.targets, p.loss, p.lse, tok / kJoin, tok / kJoin < p.M, p.V, p.ignore, lane);
+      ce_join_row<kJoin, 19>(p.part, parts, rstd, zt, t, p.loss, p.lse, row, live, p.V, p.ignore, lane);
+    }
   }
   tc_fence_before_sync();
   __syncthreads();

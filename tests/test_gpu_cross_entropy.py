@@ -351,3 +351,47 @@ def test_empty_and_refused():
     for bad in (dict(grad_loss=g.double()), dict(lse=lse[:-1]), dict(grad_loss=g[0]), dict(Wstar=W.float())):
         with pytest.raises((TypeError, ValueError, fn.FlashNormError)):
             fn.flashnorm_linear_cross_entropy_backward(**{**ok, **bad})
+
+
+@pytest.mark.parametrize("M,d", [(20, 4096), (32, 1024), (48, 4096), (40, 8192), (36, 520)])
+def test_rows_predicted_well(M, d):
+    """Rows whose target has probability 0.9 to 0.999, its weights along x so that every product of its logit has one sign.
+
+    The target's entry of dl is g (exp(l - lse) - 1). Below l = 32 the forward rounds lse twice (2^-20 each: half a step), the
+    gradient log2(e) lse once (2^-19 log2 units, 1.3e-6), the SFU's power of two is within 2^-22: together 3.5e-6, 0.35 % at
+    1 - p = 1e-3. The target's logit itself must cancel, however d products are summed: the same sum in both calls, and
+    within 2^-24 sqrt(d) of 64 bits' for a lse from there (1e-6 l at d = 8192 in the mean). The outputs' own roundings are at
+    most 2^-8. So each row of dx and each target's row of dW* is within 1 % in norm. The loss, log(1 + the others' share),
+    has that sum's roundings, 4 * 2^-24, beside the others' logits' errors, 1e-5 of itself: within 0.1 %."""
+    V, miss = 2000, (1e-1, 1e-2, 1e-3)
+    rng = np.random.default_rng(M + d)
+    x = torch.from_numpy(rng.standard_normal((M, d))).to(torch.bfloat16)
+    W = torch.from_numpy(rng.standard_normal((V, d)) * (2 / d ** 0.5)).to(torch.bfloat16)
+    t = torch.from_numpy(rng.permutation(V)[:M])
+    xd = x.double()
+    r = 1 / torch.sqrt((xd * xd).mean(dim=1, keepdim=True) + EPS)
+    base = torch.logsumexp((xd * r) @ W.double().T, dim=1)
+    for m in range(M):
+        q = miss[m % 3]
+        W[t[m]] = (xd[m] * ((base[m] + np.log((1 - q) / q)) / (r[m] * xd[m].square().sum()))).to(torch.bfloat16)
+    Wd = W.double()
+    l = (xd * r) @ Wd.T
+    lse = torch.logsumexp(l, dim=1)
+    at = (torch.arange(M), t)
+    others = torch.logsumexp(l.clone().index_put_(at, torch.tensor(-torch.inf, dtype=torch.float64)), dim=1)
+    want = torch.nn.functional.softplus(others - l[at])  # lse - l_t without their difference
+    left = -torch.expm1(-want)
+    assert ((left > 0.7 * 1e-3) & (left < 0.2)).all() and lse.max() < 32
+    loss, own = fn.flashnorm_linear_cross_entropy(x.cuda(), W.cuda(), t.cuda(), EPS)
+    assert ((loss.double().cpu() - want).abs() <= 1e-3 * want).all()
+    g = torch.ones(M)
+    dl = torch.exp(l - lse[:, None])
+    dl[at] = -left
+    dn = dl @ Wd
+    dx_w = r * (dn - xd * r * (dn * xd * r).mean(dim=1, keepdim=True))
+    dW_w = (dl.T @ (xd * r))[t]
+    for given in (own, lse.float().cuda()):
+        dx, dW = fn.flashnorm_linear_cross_entropy_backward(g.cuda(), x.cuda(), W.cuda(), t.cuda(), given, EPS)
+        for got, ref in ((dx.double().cpu(), dx_w), (dW.double().cpu()[t], dW_w)):
+            assert ((got - ref).norm(dim=1) <= 0.01 * ref.norm(dim=1)).all()
+    fn.flashnorm_check_device_error()
