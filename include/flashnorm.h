@@ -316,7 +316,8 @@ FN_API fn_status flashnorm_nvfp4_workspace_bytes(int64_t M, int64_t d, int64_t N
  *     a[m]   = max_k |x[m][k]|,   q[m][k] = rint(127 x[m][k] / a[m])  (the exact quotient, ties to even; 0 if a is 0)
  *     rho[m] = a[m] / 127 / sqrt(mean_k x[m][k]^2 + eps)   (norm = 0: a[m] / 127)
  *     y[m][n] = (sum_k q[m][k] Q[n][k]) rho[m] s[n],   GLU: silu(gate) * up of those values.
- *   The deferred norm is free: 1/rms joins the row scale. A row with an infinity or a NaN is written as NaN.
+ *   The deferred norm is free: 1/rms joins the row scale. A row with an infinity or a NaN is written as NaN. A channel whose
+ *   W* holds one has s = NaN and Q = 0, which makes its outputs NaN.
  * flashnorm_fold_weights_int8: W bf16 [d, N] row-major, g bf16 [d] -> Q int8 [N, d] K-major and scales fp32 [N]. glu as
  *   for flashnorm_fold_weights (N = 2F; rows and their scales interleaved in blocks of FN_GLU_BLOCK).
  * flashnorm_linear_int8: x bf16 [M, d] -> y [M, N] of out_dtype. norm = 0 leaves 1/rms out (a projection that no norm

@@ -3,7 +3,8 @@
 //
 //     a[m]   = max_k |x[m, k]|,   q[m, k] = round(127 x[m, k] / a[m])        (ties to even; 0 for a row of zeros)
 //     rho[m] = a[m] / 127 / sqrt(mean_k x[m, k]^2 + eps)                      (no norm: a[m] / 127)
-//     s[n]   = max_k |g[k] W[k, n]| / 127,   Q[n, k] = round(g[k] W[k, n] / s[n])   (s = 1 for a channel of zeros)
+//     s[n]   = max_k |g[k] W[k, n]| / 127,   Q[n, k] = round(g[k] W[k, n] / s[n])   (s = 1 for a channel of zeros, NaN for
+//                                                                                   one that is not finite)
 //     y[m, n] = rho[m] s[n] sum_k q[m, k] Q[n, k]
 // The deferred normalisation of "FlashNorm: Fast Normalization for Transformers" (Abstract, item ii) costs nothing
 // here: 1/rms is a row scalar, and so is the scale that any per-token quantization multiplies the product with.
@@ -24,21 +25,24 @@ namespace fn {
 // ---------------------------------------------------------------------------------------------- weights (offline)
 
 // s[row] of every output channel: 32 channels per block, eight k slices of each joined in shared memory. For GLU the
-// channel's row is the interleaved one (fold_dst_row).
+// channel's row is the interleaved one (fold_dst_row). Magnitudes are compared as bits, where NaN orders above infinity and
+// both above every number: a channel that holds either gets the scale NaN (and, x / NaN being NaN, zero codes), so that it
+// shows in what is computed from it, as a row of x with such a value does.
 __global__ void __launch_bounds__(256) k_int8_scales(const uint16_t* __restrict__ W, const uint16_t* __restrict__ g,
                                                      float* __restrict__ scales, int d, int N, int glu) {
-  __shared__ float part[8][32];
+  __shared__ uint32_t part[8][32];
   grid_dep_wait();
   const int n = blockIdx.x * 32 + (threadIdx.x & 31), sl = threadIdx.x >> 5;
-  float amax = 0.0f;
+  uint32_t amax = 0;
   if (n < N)
     for (int k = sl; k < d; k += 8)
-      amax = fmaxf(amax, fabsf(bf16lo_to_f32(g[k]) * bf16lo_to_f32(W[static_cast<size_t>(k) * N + n])));
+      amax = max(amax, __float_as_uint(bf16lo_to_f32(g[k]) * bf16lo_to_f32(W[static_cast<size_t>(k) * N + n])) & 0x7FFFFFFFu);
   part[sl][threadIdx.x & 31] = amax;
   __syncthreads();
   if (sl == 0 && n < N) {
-    for (int i = 1; i < 8; ++i) amax = fmaxf(amax, part[i][threadIdx.x]);
-    scales[fold_dst_row(n, N / 2, glu != 0)] = amax > 0.0f ? __fdiv_rn(amax, 127.0f) : 1.0f;
+    for (int i = 1; i < 8; ++i) amax = max(amax, part[i][threadIdx.x]);
+    const float a = __uint_as_float(amax >= 0x7F800000u ? 0x7FC00000u : amax);
+    scales[fold_dst_row(n, N / 2, glu != 0)] = a == 0.0f ? 1.0f : __fdiv_rn(a, 127.0f);
   }
 }
 

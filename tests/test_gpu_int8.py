@@ -227,3 +227,39 @@ def test_int8_refuses():
         with pytest.raises((TypeError, ValueError, fn.FlashNormError)):
             fn.flashnorm_linear_int8(**{**dict(x=x, Q=Q, scales=s, eps=1e-5), **bad})
     assert fn.flashnorm_linear_int8(x[:0], Q, s, 1e-5).shape == (0, 32)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("glu", [False, True])
+@pytest.mark.parametrize("M", [3, 40])
+def test_fold_of_weights_that_are_not_finite(M, glu, value):
+    """A channel whose folded weights hold a NaN or an infinity has scale NaN and zero codes, its outputs are NaN, and the
+    others keep their bits; a gain that is not finite is in every channel."""
+    rng = np.random.default_rng(M)
+    d, N = 208, 96
+    W = torch.from_numpy(rng.standard_normal((d, N)) / d ** 0.5).to(torch.bfloat16)
+    g = torch.from_numpy(rng.uniform(0.5, 1.5, d)).to(torch.bfloat16)
+    x = torch.from_numpy(rng.standard_normal((M, d))).to(torch.bfloat16).cuda()
+    call = fn.flashnorm_glu_int8 if glu else fn.flashnorm_linear_int8
+    dst = glu_dst_rows(N // 2) if glu else np.arange(N)
+    Q, s = fn.flashnorm_fold_weights_int8(W.cuda(), g.cuda(), glu=glu)
+    want = call(x, Q, s, 1e-5)
+    bad_n = [0, 37, N - 1]
+    Wb = W.clone()
+    for n, k in zip(bad_n, (0, 100, d - 1)):
+        Wb[k, n] = value
+    Qb, sb = fn.flashnorm_fold_weights_int8(Wb.cuda(), g.cuda(), glu=glu)
+    rows = torch.zeros(N, dtype=torch.bool)
+    rows[[int(dst[n]) for n in bad_n]] = True
+    rows = rows.cuda()
+    assert torch.equal(sb.isnan(), rows) and (Qb[rows] == 0).all()
+    assert torch.equal(sb[~rows], s[~rows]) and torch.equal(Qb[~rows], Q[~rows])
+    cols = torch.zeros(want.shape[1], dtype=torch.bool, device="cuda")
+    cols[[n % want.shape[1] for n in bad_n]] = True  # GLU: columns of a gate or an up channel
+    y = call(x, Qb, sb, 1e-5)
+    assert y[:, cols].isnan().all() and torch.equal(y[:, ~cols], want[:, ~cols])
+    gb = g.clone()
+    gb[5] = value
+    Qb, sb = fn.flashnorm_fold_weights_int8(W.cuda(), gb.cuda(), glu=glu)
+    assert sb.isnan().all() and (Qb == 0).all() and call(x, Qb, sb, 1e-5).isnan().all()
+    fn.flashnorm_check_device_error()
