@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kI8DecThreads, 2)
     const int t = static_cast<int>(threadIdx.x) - 64;
     const int row = q * 32 + lane;  // row of Q within the slab
     grid_dep_wait();
-    bool ok = mbar_wait(acc_full, 0, abort_flag);
+    bool ok = __all_sync(0xffffffffu, mbar_wait(acc_full, 0, abort_flag));
     int v[kI8Tok];
 #pragma unroll
     for (int j = 0; j < kI8Tok; ++j) v[j] = 0;

@@ -271,11 +271,11 @@ __global__ void __launch_bounds__(kI8cThreads, 2)
     // ------------------------------------------------------------------ partial sums to the ranks that finish them
     const int q = warp & 3, half = w >> 2;
     const int row = q * 32 + lane;  // of the slab
-    const bool ok = mbar_wait(acc_full, 0, abort_flag);
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(acc_full, 0, abort_flag));
     int v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = 0;
-    if (__all_sync(0xffffffffu, ok) && 8 * half < p.M) {
+    if (ok && 8 * half < p.M) {
       tc_fence_after_sync();
       const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + 8 * half;
       uint32_t r[4][8];

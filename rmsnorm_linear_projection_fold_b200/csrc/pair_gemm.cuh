@@ -484,7 +484,7 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tm_a0, const C
     const uint32_t leader_acc_empty1 = dsmem_addr(&acc_empty[1], 0);
     int acc = 0;
     uint32_t acc_ph = 0;
-    // One tile: false once a wait gave up.
+    // One tile: false, for the whole warp, once a wait gave up.
     auto finish = [&](auto* job, const PairGemmParams& p, const auto& ep, const PgPlan& pl, int turn) {
       using Epi = typename std::remove_pointer_t<decltype(job)>::Epi;
       PgTile tile;
@@ -501,7 +501,7 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tm_a0, const C
       Epi epi(ep, p, tile, lane);  // row parameters are on their way while the MMAs finish
       for (tile.chunk = 0; tile.chunk < tile.chunks; ++tile.chunk) {
         tile.t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * 256);
-        if (!mbar_wait_cluster(&acc_full[acc], acc_ph, abort_flag)) return false;
+        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&acc_full[acc], acc_ph, abort_flag))) return false;
         tc_fence_after_sync();
         epi.run(ep, p, tile, lane);
         tc_fence_before_sync();
