@@ -73,8 +73,8 @@ __global__ void __launch_bounds__(kI8cThreads, 2)
   int* red = reinterpret_cast<int*>(sX + p.max_kb * code_bytes);            // [rank][token of mine][128]
   uint2* stat = reinterpret_cast<uint2*>(red + kI8cRedSlots * 128);         // [rank][16]: magnitude bits, sum of squares
   float* rho = reinterpret_cast<float*>(stat + kI8cMaxRanks * 16);          // [16]
-  uint32_t* failed = reinterpret_cast<uint32_t*>(rho + 16);                 // [rank]
-  uint64_t* full = reinterpret_cast<uint64_t*>(failed + kI8cMaxRanks);      // [16 at most]
+  uint32_t* failed = reinterpret_cast<uint32_t*>(rho + 16);                 // [rank][8]: by each of its epilogue warps
+  uint64_t* full = reinterpret_cast<uint64_t*>(failed + kI8cMaxRanks * 8);  // [16 at most]
   uint64_t* empty = full + 16;
   uint64_t* acc_full = empty + 16;
   uint64_t* codes_ready = acc_full + 1;
@@ -299,8 +299,7 @@ __global__ void __launch_bounds__(kI8cThreads, 2)
       dsmem_st_b32(dsmem_addr(red + (rank * per + m / ranks) * kI8Rows + row, static_cast<uint32_t>(m % ranks)),
                    static_cast<uint32_t>(v[j]));
     }
-    if (w == 0 && lane < ranks)
-      dsmem_st_b32(dsmem_addr(failed + rank, static_cast<uint32_t>(lane)), *abort_flag != 0 || !ok ? 1u : 0u);
+    if (lane < ranks) dsmem_st_b32(dsmem_addr(failed + rank * 8 + w, static_cast<uint32_t>(lane)), *abort_flag != 0 || !ok ? 1u : 0u);
   }
   tc_fence_before_sync();
   cluster_sync_all();  // partial sums are in place, and no CTA is written to any more
@@ -309,8 +308,7 @@ __global__ void __launch_bounds__(kI8cThreads, 2)
   if (warp >= 2) {
     const int w = warp - 2, q = warp & 3, half = w >> 2;
     const int row = q * 32 + lane, n = n0 + row;
-    bool bad = false;
-    for (int r = 0; r < ranks; ++r) bad |= failed[r] != 0;
+    const bool bad = __any_sync(0xffffffffu, (lane < 8 * ranks && failed[lane] != 0) || (lane + 32 < 8 * ranks && failed[lane + 32] != 0));
     // a sum that a failed wait left incomplete is written as NaN (the status word reports the timeout)
     const float sc = bad ? __int_as_float(0x7fc00000) : row < p.rows && n < p.n_rows ? __ldg(p.scale + n) : 0.f;
     // rows 32b + j (gate) and 32b + 16 + j (up) are lanes j and j + 16 of one warp

@@ -48,3 +48,11 @@ def test_the_reader_sees_an_unvoted_wait():
 def test_waits_of_whole_warps_are_voted_on(name):
     code = _code(name)
     assert "mbar_wait" in code and _unvoted(code) == []
+
+
+def test_every_epilogue_warp_of_the_cluster_decode_reports_its_own_wait():
+    """A rank's partial sums come from eight warps, whose waits may end differently: each has a word of its own, and a sum counts
+    as incomplete if any of them is set."""
+    code = _code("decode_int8_cluster.cuh")
+    assert re.search(r"dsmem_addr\(failed \+ rank \* 8 \+ w,", code)
+    assert re.search(r"failed \+ kI8cMaxRanks \* 8\b", code) and "lane + 32 < 8 * ranks" in code
