@@ -37,7 +37,7 @@
  *     returns early instead of hanging. The outputs of such a call are not valid; the tensor-core
  *     decode kernel writes the outputs that a failed wait affects as NaN (its K-split partial sums
  *     from the CTA that gave up are NaN), the prefill kernels leave the tiles they did not finish
- *     unwritten.
+ *     unwritten, the cross entropy's loss and lse are NaN.
  *   - Host threads: entry points may be called from several threads. flashnorm_last_error is kept per
  *     thread. The one-time per-device setup of the first calls on a device (kernel shared-memory
  *     attributes, the SM count) sets the same values whoever performs it, so concurrent first calls

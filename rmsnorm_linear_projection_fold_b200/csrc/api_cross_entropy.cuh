@@ -55,7 +55,7 @@ struct CePlan {
   int n_tiles;     // column tiles of a full piece
   int ksplit;      // K ranges of dx's product, and of dW*'s where it goes through planes
   int dw_ksplit;
-  int64_t arrived, rstd, part, tlogit;               // forward
+  int64_t arrived, failed, rstd, part, tlogit;       // forward (arrived, tlogit: few rows; failed: more)
   int64_t n_live, rows, rank_of, target, u, ct, hits, xc, P, acc, dw_acc, bytes;  // backward (and part)
 };
 
@@ -114,7 +114,7 @@ CePlan ce_plan(int64_t M, int64_t d, int64_t V, bool backward, int sms) {
   plan_pair_gemm(&g, M, c.piece, (d + 63) / 64, sms, 32);
   c.n_tiles = g.num_n_tiles;
   if (!backward) {
-    c.arrived = 0;
+    c.arrived = c.failed = 0;
     c.rstd = 256;
     c.part = c.rstd + round_up(4 * M, 256);
     if (M <= kCeSmallRows) {
@@ -167,9 +167,9 @@ fn_status check_ce_call(const void* x, const void* w, const void* targets, const
   return check_ptr(workspace, "workspace");
 }
 
-fn_status launch_rstd(const void* x, float* rstd, unsigned* arrived, int64_t M, int64_t d, float eps, cudaStream_t s) {
+fn_status launch_rstd(const void* x, float* rstd, unsigned* zero, int64_t M, int64_t d, float eps, cudaStream_t s) {
   cudaError_t e = launch_kernel(fn::k_row_rstd, dim3(static_cast<unsigned>((M + 7) / 8)), dim3(256), 0, s, 1,
-                                static_cast<const uint16_t*>(x), rstd, arrived, static_cast<int>(M), static_cast<int>(d), eps);
+                                static_cast<const uint16_t*>(x), rstd, zero, static_cast<int>(M), static_cast<int>(d), eps);
   return e == cudaSuccess ? FN_OK : cuda_fail(e, "row statistics launch");
 }
 
@@ -254,10 +254,11 @@ fn_status flashnorm_linear_cross_entropy(const void* x, const void* Wstar, const
   plan_pair_gemm(&p, M, V, (d + 63) / 64, sms, 32);
   p.kchunk = kCeFwdChunk;
   p.early = fn::PG_EARLY_AB;  // neither operand depends on the row statistics
+  p.failed = reinterpret_cast<unsigned*>(base + c.failed);
   CUtensorMap tx, tw;
   if ((st = make_k_map(&tx, x, d, M, d, 128)) != FN_OK) return st;
   if ((st = make_k_map(&tw, Wstar, d, V, d, p.bn / 2)) != FN_OK) return st;
-  if ((st = launch_rstd(x, rstd, nullptr, M, d, eps, s)) != FN_OK) return st;
+  if ((st = launch_rstd(x, rstd, p.failed, M, d, eps, s)) != FN_OK) return st;
   const char* what = "cross entropy GEMM";
   st = p.num_kb > kCeFwdChunk
            ? launch_pair_gemm<fn::PG_BF16, fn::PgJob<false, false, fn::CeFwdEpi<true>>>(tx, tw, p, ep, sms, dev, s, what)
@@ -265,8 +266,8 @@ fn_status flashnorm_linear_cross_entropy(const void* x, const void* Wstar, const
   if (st != FN_OK) return st;
   cudaError_t e = launch_kernel(fn::k_ce_join, dim3(static_cast<unsigned>((M + 7) / 8)), dim3(256), 0, s, 1,
                                 static_cast<const float2*>(ep.part), ep.rstd, static_cast<const uint16_t*>(x),
-                                static_cast<const uint16_t*>(Wstar), ep.targets, static_cast<float*>(loss),
-                                static_cast<float*>(lse), p.M, static_cast<int>(d), p.N, kCeFwdParts * p.num_n_tiles,
+                                static_cast<const uint16_t*>(Wstar), ep.targets, static_cast<const unsigned*>(p.failed),
+                                static_cast<float*>(loss), static_cast<float*>(lse), p.M, static_cast<int>(d), p.N, kCeFwdParts * p.num_n_tiles,
                                 static_cast<long long>(ignore_index));
   return e == cudaSuccess ? FN_OK : cuda_fail(e, "cross entropy join launch");
 }

@@ -46,13 +46,13 @@ __device__ __forceinline__ float ex2(float v) {
   return e;
 }
 
-// r[m] = 1/sqrt(mean(x[m]^2) + eps), one warp per row. Also zeroes `arrived` (not null: the arrival counter of the kernel that
-// follows).
+// r[m] = 1/sqrt(mean(x[m]^2) + eps), one warp per row. Also zeroes the word `zero` of the kernel that follows (its arrivals, or
+// whether it failed).
 __global__ void __launch_bounds__(256) k_row_rstd(const uint16_t* __restrict__ x, float* __restrict__ rstd,
-                                                  unsigned* __restrict__ arrived, int M, int K, float eps) {
+                                                  unsigned* __restrict__ zero, int M, int K, float eps) {
   grid_dep_wait();
   grid_dep_launch();
-  if (arrived != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *arrived = 0u;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *zero = 0u;
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (row >= M) return;
   const uint4* src = reinterpret_cast<const uint4*>(x + static_cast<size_t>(row) * K);
@@ -258,18 +258,22 @@ __device__ __forceinline__ void ce_join_row(const float2* part, int parts, float
 }
 
 // A warp per row. x, W* and the targets are in place before the product starts (the row statistics' pass waited for them), so
-// the target's logit is taken before the wait.
+// the target's logit is taken before the wait. A product that gave up (*failed) has left pairs unwritten: NaN then, as the status
+// word reports.
 __global__ void __launch_bounds__(256) k_ce_join(const float2* __restrict__ part, const float* __restrict__ rstd,
                                                  const uint16_t* __restrict__ x, const uint16_t* __restrict__ W,
-                                                 const long long* __restrict__ targets, float* __restrict__ loss,
-                                                 float* __restrict__ lse, int M, int K, int V, int parts, long long ignore) {
+                                                 const long long* __restrict__ targets, const unsigned* failed,
+                                                 float* __restrict__ loss, float* __restrict__ lse, int M, int K, int V,
+                                                 int parts, long long ignore) {
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const long long t = row < M ? __ldcg(targets + row) : ignore;
   const float zt = row < M && target_is_class(t, V)
                        ? ce_row_dot(x + static_cast<size_t>(row) * K, W + static_cast<size_t>(t) * K, K, lane) : 0.f;
   grid_dep_wait();
   grid_dep_launch();
+  const unsigned gave_up = __ldcg(failed);  // looked at last: its load runs beside those of the pairs
   ce_join_row<32, 10>(part, parts, row < M ? __ldcg(rstd + row) : 0.f, zt, t, loss, lse, row, row < M, V, ignore, lane);
+  if (gave_up != 0u && row < M && lane == 0) loss[row] = lse[row] = __int_as_float(0x7fc00000);
 }
 
 // ---------------------------------------------------------------------------------------------- backward

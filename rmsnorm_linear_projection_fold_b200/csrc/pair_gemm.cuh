@@ -65,6 +65,7 @@ struct PairGemmParams {
   const int* live;  // null, or a count on the device that replaces M (at most M) or num_kb (at most so many stages)
   int b_blocks;     // MN-major B: its map has blocks of 64 columns as a third dimension, one copy per stage
   int extra;        // job 1: items that a pair with one item less of job 0 takes first, in exchange
+  unsigned* failed;  // null, or a word that is set to 1 if tiles are left unfinished because a wait ran out
 };
 
 // Operands that may be fetched before the previous kernel has completed. That kernel must itself have waited for all
@@ -524,6 +525,7 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tm_a0, const C
       else
         ok = finish(static_cast<J0*>(nullptr), p0, ep0, plan0, turn);
     }
+    if (!ok && lane == 0 && p0.failed != nullptr) atomicExch(p0.failed, 1u);
   }
 
   // ------------------------------------------------------------------ teardown

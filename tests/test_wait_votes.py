@@ -56,3 +56,14 @@ def test_every_epilogue_warp_of_the_cluster_decode_reports_its_own_wait():
     code = _code("decode_int8_cluster.cuh")
     assert re.search(r"dsmem_addr\(failed \+ rank \* 8 \+ w,", code)
     assert re.search(r"failed \+ kI8cMaxRanks \* 8\b", code) and "lane + 32 < 8 * ranks" in code
+
+
+def test_a_loss_whose_product_gave_up_is_not_joined_from_what_lies_in_the_workspace():
+    """The CTA-pair product sets a word of the workspace when it leaves tiles unfinished; the row pass before it clears that word and
+    the join after it writes NaN where it is set."""
+    product, head, host = (_code(n) for n in ("pair_gemm.cuh", "cross_entropy.cuh", "api_cross_entropy.cuh"))
+    assert re.search(r"if \(!ok && lane == 0 && p0\.failed != nullptr\) atomicExch\(p0\.failed, 1u\)", product)
+    join = head[head.index(" k_ce_join("):head.index("struct __align__(16) CeRow")]
+    assert re.search(r"grid_dep_wait\(\);.* gave_up = __ldcg\(failed\);.*ce_join_row<.*if \(gave_up != 0u[^;]*\) loss\[row\] = lse\[row\] = "
+                     r"__int_as_float\(0x7fc00000\)", join, re.S)
+    assert "launch_rstd(x, rstd, p.failed," in host
