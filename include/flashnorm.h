@@ -18,7 +18,7 @@
  *
  * Conventions shared by every entry point
  *   - All tensor pointers are caller-owned DEVICE memory on the current device; the library never
- *     allocates, frees or keeps them. Pointers must be 16-byte aligned.
+ *     allocates, frees or keeps them. Pointers must be 16-byte aligned, unless an entry point asks for less.
  *   - Element types: activations, weights, gains and the unfused intermediate are bf16 (stored as
  *     uint16 bit patterns); outputs are bf16 or fp32 as `out_dtype` says. All arithmetic is fp32
  *     with one round-to-nearest-even conversion per bf16 result.
@@ -363,7 +363,8 @@ FN_API fn_status flashnorm_int8_workspace_bytes(int64_t M, int64_t d, int64_t N,
  *   device, written to *bytes; bounded by a piece of the vocabulary, not the whole. Caller-owned, 16-byte aligned,
  *   contents irrelevant before and after; calls whose kernels may overlap on the GPU must not share one. A smaller one
  *   returns FN_ERR_INVALID_ARG.
- * Constraints: d % 8 == 0; any M and V.
+ * Constraints: d % 8 == 0; any M and V. targets, g, loss and lse need no more than their elements' alignment (8 and 4
+ * bytes): labels shifted by one are a slice that starts 8 bytes on.
  */
 FN_API fn_status flashnorm_linear_cross_entropy(const void* x, const void* Wstar, const void* targets, void* loss,
                                                 void* lse, int64_t M, int64_t d, int64_t V, float eps,

@@ -161,9 +161,9 @@ fn_status check_ce_call(const void* x, const void* w, const void* targets, const
   if (workspace_bytes < 0) return fail(FN_ERR_INVALID_ARG, "workspace_bytes < 0");
   if ((st = check_ptr(x, "x")) != FN_OK) return st;
   if ((st = check_ptr(w, "W*")) != FN_OK) return st;
-  if ((st = check_ptr(targets, "targets")) != FN_OK) return st;
-  if ((st = check_ptr(a, an)) != FN_OK) return st;
-  if ((st = check_ptr(b, bn)) != FN_OK) return st;
+  if ((st = check_vec(targets, "targets", 8)) != FN_OK) return st;
+  if ((st = check_vec(a, an, 4)) != FN_OK) return st;
+  if ((st = check_vec(b, bn, 4)) != FN_OK) return st;
   return check_ptr(workspace, "workspace");
 }
 

@@ -216,6 +216,13 @@ fn_status check_ptr(const void* p, const char* name) {
   return FN_OK;
 }
 
+// The same for a vector that kernels read one element at a time: any slice of it will do.
+fn_status check_vec(const void* p, const char* name, unsigned element_bytes) {
+  if (p == nullptr) return fail(FN_ERR_INVALID_ARG, "%s is NULL", name);
+  if (reinterpret_cast<uintptr_t>(p) % element_bytes != 0) return fail(FN_ERR_ALIGN, "%s is not aligned to its elements", name);
+  return FN_OK;
+}
+
 constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1;
 
 fn_status check_common(const void* x, const void* w, const void* y, int64_t M, int64_t d, float eps, int out_dtype) {

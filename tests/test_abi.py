@@ -424,3 +424,18 @@ def test_cross_entropy_validation(lib):
     assert size(4, 64, 100, 2, out) == fn.FN_ERR_INVALID_ARG
     assert size(4, 60, 100, 0, out) == fn.FN_ERR_INVALID_ARG
     assert size(0, 64, 100, 1, out) == fn.FN_OK and n.value == 0
+
+
+def test_cross_entropy_takes_slices_of_its_vectors(lib):
+    """targets, loss, lse and g are read and written one element at a time: a slice that starts on an element is no misaligned
+    pointer (here the call goes on to the next check, of the workspace), one that does not is."""
+    fwd, bwd = lib.flashnorm_linear_cross_entropy, lib.flashnorm_linear_cross_entropy_backward
+
+    def at(n):
+        return ctypes.c_void_p((1 << 20) + n)
+
+    assert fwd(P, P, at(8), at(4), at(12), 4, 64, 100, 1e-6, -100, NULL, 0, NULL) == fn.FN_ERR_INVALID_ARG
+    assert bwd(at(4), P, P, at(8), at(12), P, P, 4, 64, 100, 1e-6, -100, NULL, 0, NULL) == fn.FN_ERR_INVALID_ARG
+    for bad in ((at(4), P, P), (P, at(2), P), (P, P, at(6))):
+        assert fwd(P, P, *bad, 4, 64, 100, 1e-6, -100, NULL, 0, NULL) == fn.FN_ERR_ALIGN
+        assert bwd(bad[1], P, P, bad[0], bad[2], P, P, 4, 64, 100, 1e-6, -100, NULL, 0, NULL) == fn.FN_ERR_ALIGN

@@ -395,3 +395,23 @@ def test_rows_predicted_well(M, d):
         for got, ref in ((dx.double().cpu(), dx_w), (dW.double().cpu()[t], dW_w)):
             assert ((got - ref).norm(dim=1) <= 0.01 * ref.norm(dim=1)).all()
     fn.flashnorm_check_device_error()
+
+
+@pytest.mark.parametrize("M", [20, 75])
+def test_shifted_labels_and_sliced_vectors(M):
+    """Next-token labels are the tokens from the second on: a slice 8 bytes into its storage. It, and slices of g and lse that
+    start 4 bytes in, give the bits of their aligned copies."""
+    d, V = 72, 1003
+    x, W, t, g = _draw(M, d, V, seed=4)
+    x, W, t, g = (v.cuda() for v in (x, W, t, g))
+    tokens = torch.cat([t[:1], t])[None]
+    labels = tokens[:, 1:].contiguous().view(-1)
+    assert labels.data_ptr() % 16 == 8
+    loss, lse = fn.flashnorm_linear_cross_entropy(x, W, t, EPS)
+    again = fn.flashnorm_linear_cross_entropy(x, W, labels, EPS)
+    assert torch.equal(again[0], loss) and torch.equal(again[1], lse)
+    dx, dW = fn.flashnorm_linear_cross_entropy_backward(g, x, W, t, lse, EPS)
+    g1, lse1 = torch.cat([g[:1], g])[1:], torch.cat([lse[:1], lse])[1:]
+    again = fn.flashnorm_linear_cross_entropy_backward(g1, x, W, labels, lse1, EPS)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dW)
+    fn.flashnorm_check_device_error()
