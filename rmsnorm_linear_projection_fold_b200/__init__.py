@@ -721,6 +721,8 @@ def flashnorm_rope_table_scaled(max_pos: int, rot_dim: int, base: float = 10000.
         raise ValueError("max_pos must be positive, rot_dim positive and even")
     if out is None:
         dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        if dev.type != "cuda":
+            raise ValueError(f"device must be a CUDA device, got {dev}")
         out = torch.empty(max_pos, rot_dim // 2, 2, dtype=torch.float32, device=dev)
     else:
         _need(out, "out", torch.float32)
