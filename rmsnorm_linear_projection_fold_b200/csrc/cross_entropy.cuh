@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(256, 2) k_ce_pack(const uint16_t* __restrict__
   __shared__ int counts[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   auto live_at = [&](int m) {
-    const long long t = __ldg(targets + m);
+    const long long t = __ldcg(targets + m);
     return t != ignore && target_is_class(t, V);
   };
   const int b0 = static_cast<int>(blockIdx.x) * rows_per_block;
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(256, 2) k_ce_pack(const uint16_t* __restrict__
       held[i] = lane + 32 * i < chunks ? __ldcg(src + lane + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
     if (target_is_class(t, V)) load_w(t, 0);
   };
-  long long t = m0 < M ? __ldg(targets + m0) : ignore;
+  long long t = m0 < M ? __ldcg(targets + m0) : ignore;
   if (m0 < M) load_row(m0, t);
   int n = 0;
 #pragma unroll 8
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(256, 2) k_ce_pack(const uint16_t* __restrict__
   int rank = base + count(b0, min(m0, M));
   long long t_next;
   for (int m = m0; m < min(m0 + per_warp, M); ++m, t = t_next) {
-    t_next = m + 1 < M ? __ldg(targets + m + 1) : ignore;
+    t_next = m + 1 < M ? __ldcg(targets + m + 1) : ignore;
     const bool live = t != ignore && target_is_class(t, V);
     if (lane == 0) rank_of[m] = live ? rank : t == ignore ? kCeIgnored : kCeBad;
     if (!live) continue;
@@ -396,8 +396,8 @@ __global__ void __launch_bounds__(256, 2) k_ce_pack(const uint16_t* __restrict__
     if (lane == 0) {
       CeRow r;
       r.rstd = 1.0f / sqrtf(ss / static_cast<float>(K) + eps);
-      r.nlse2 = -__ldg(lse + m) * kLog2e;
-      r.g = __ldg(g + m);
+      r.nlse2 = -__ldcg(lse + m) * kLog2e;
+      r.g = __ldcg(g + m);
       r.target = static_cast<int>(t);
       rows[rank] = r;
       target[rank] = r.target;

@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kI8cThreads, 2)
     const int row = q * 32 + lane, n = n0 + row;
     const bool bad = __any_sync(0xffffffffu, (lane < 8 * ranks && failed[lane] != 0) || (lane + 32 < 8 * ranks && failed[lane + 32] != 0));
     // a sum that a failed wait left incomplete is written as NaN (the status word reports the timeout)
-    const float sc = bad ? __int_as_float(0x7fc00000) : row < p.rows && n < p.n_rows ? __ldg(p.scale + n) : 0.f;
+    const float sc = bad ? __int_as_float(0x7fc00000) : row < p.rows && n < p.n_rows ? __ldcg(p.scale + n) : 0.f;
     // rows 32b + j (gate) and 32b + 16 + j (up) are lanes j and j + 16 of one warp
     const int col = GLU ? ((n0 + q * 32) >> 1) + (lane & 15) : n;
     const bool mine = row < p.rows && col < p.n_out && (!GLU || lane < 16);

@@ -28,8 +28,8 @@ namespace fn {
 // channel's row is the interleaved one (fold_dst_row). Magnitudes are compared as bits, where NaN orders above infinity and
 // both above every number: a channel that holds either gets the scale NaN (and, x / NaN being NaN, zero codes), so that it
 // shows in what is computed from it, as a row of x with such a value does.
-__global__ void __launch_bounds__(256) k_int8_scales(const uint16_t* __restrict__ W, const uint16_t* __restrict__ g,
-                                                     float* __restrict__ scales, int d, int N, int glu) {
+__global__ void __launch_bounds__(256) k_int8_scales(const uint16_t* W, const uint16_t* g,
+                                                     float* scales, int d, int N, int glu) {
   __shared__ uint32_t part[8][32];
   grid_dep_wait();
   const int n = blockIdx.x * 32 + (threadIdx.x & 31), sl = threadIdx.x >> 5;
@@ -47,8 +47,8 @@ __global__ void __launch_bounds__(256) k_int8_scales(const uint16_t* __restrict_
 }
 
 // The codes, K-major: one 64 x 64 tile of W per block through shared memory, as k_fold does. d % 16 == 0, N % 8 == 0.
-__global__ void __launch_bounds__(256) k_fold_int8(const uint16_t* __restrict__ W, const uint16_t* __restrict__ g,
-                                                   const float* __restrict__ scales, int8_t* __restrict__ Q, int d,
+__global__ void __launch_bounds__(256) k_fold_int8(const uint16_t* W, const uint16_t* g,
+                                                   const float* scales, int8_t* Q, int d,
                                                    int N, int glu) {
   __shared__ float tile[kFoldTile][kFoldTile + 1];  // [n][k]
   const int k0 = blockIdx.y * kFoldTile, n0 = blockIdx.x * kFoldTile;
@@ -160,8 +160,10 @@ struct Int8Row {
 };
 
 // LPR threads per row, 256 / LPR rows per block; a thread keeps up to 4 x 8 elements of its row in registers, and a
-// longer row's remainder is read a second time. x is read from L2, here and in the other row passes: the kernel before may
-// have written it in place, and its own reads may have left older lines in this SM's L1. Also zeroes the `nzero` words at `zero`, the arrival
+// longer row's remainder is read a second time. x is read once, so past the L1, here and in the other row passes. What the
+// kernel before may have written is read behind griddepcontrol.wait, which makes it visible to coherent loads; this kernel starts
+// before that one ends, so such data is not constant for its lifetime and never read through the non-coherent path (__ldg).
+// Also zeroes the `nzero` words at `zero`, the arrival
 // counters of a decode kernel that follows.
 // Bound: instruction issue before HBM (2048 x 4096: 25 MB in 10.3 us, launch included; with a conversion and a check per
 // code, 14 us). More blocks per SM with fewer registers were slower (11 to 16 us).

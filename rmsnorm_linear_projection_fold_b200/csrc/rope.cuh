@@ -34,14 +34,14 @@ struct RopeVec {
   uint4 w;
   __device__ __forceinline__ void load(const T* p) {
     if constexpr (kBytes == 16) {
-      w = *reinterpret_cast<const uint4*>(p);
+      w = __ldcg(reinterpret_cast<const uint4*>(p));
     } else if constexpr (kBytes == 8) {
-      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      const uint2 v = __ldcg(reinterpret_cast<const uint2*>(p));
       w.x = v.x, w.y = v.y;
     } else if constexpr (kBytes == 4) {
-      w.x = *reinterpret_cast<const uint32_t*>(p);
+      w.x = __ldcg(reinterpret_cast<const uint32_t*>(p));
     } else {
-      w.x = *reinterpret_cast<const uint16_t*>(p);
+      w.x = __ldcg(reinterpret_cast<const uint16_t*>(p));
     }
   }
   __device__ __forceinline__ void store(T* p) const {
@@ -83,7 +83,9 @@ struct RopeVec {
 // Bound: HBM (each feature read and written once). A (cos, sin) pair is twice to four times as many bytes as the
 // feature it turns, so a thread keeps the pairs of its unit in registers and serves several heads with them. All heads of a
 // batch are loaded before any is stored (128 bytes in flight per thread): x and y may be the same memory, so the compiler
-// cannot reorder them itself. 8192 x 96 x 128 bf16: 403 MB in 68 us (83 with one load in flight); 8192 x 48 heads of
+// cannot reorder them itself. x is read once, past the L1; positions and table by
+// many threads of an SM, with plain (coherent) loads through it (positions past the L1: 71 us): the kernel before may have written
+// any of them. 8192 x 96 x 128 bf16: 403 MB in 68 us (83 with one load in flight); 8192 x 48 heads of
 // 108 features, 72 rotated, in accesses of four: 37 us (77 feature by feature).
 template <typename T, int VEC, bool HALF>
 __global__ void __launch_bounds__(256) k_rope(RopeParams p) {
@@ -136,7 +138,7 @@ __global__ void __launch_bounds__(256) k_rope(RopeParams p) {
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
         // a unit that straddles rot_dim (interleaved): its last pairs are carried over and have no table entry
-        const float2 v = i0 + j < half ? __ldg(row + i0 + j) : make_float2(1.f, 0.f);
+        const float2 v = i0 + j < half ? row[i0 + j] : make_float2(1.f, 0.f);
         c[j] = v.x;
         s[j] = p.sign * v.y;
       }

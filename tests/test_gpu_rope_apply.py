@@ -180,3 +180,26 @@ def test_rope_refuses():
             fn.flashnorm_rope(**{**dict(x=x, rope_cs=cs, positions=pos), **bad})
     with pytest.raises(fn.FlashNormError):  # an output whose heads share their place
         fn.flashnorm_rope(x, cs, pos, out=torch.empty(4, 1, 32, dtype=torch.bfloat16, device="cuda").expand(4, 2, 32))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("hd,rot,layout", [(20, 20, "half"), (18, 12, "interleaved"), (36, 36, "half"), (24, 16, "interleaved")])
+def test_rotations_in_place_back_to_back(hd, rot, layout, dtype):
+    """Each call starts while the one before still writes the same buffer; rows are no multiples of a cache line, so blocks share
+    lines. Forty rotations, the table written again before each fourth, give the bits of the same calls with a wait between."""
+    M, H = 3001, 5
+    x, pos, _ = _inputs(M, H, hd, rot, 61, dtype, seed=hd)
+    cs = torch.empty(61, rot // 2, 2, device="cuda")
+
+    def turn(y, between):
+        for i in range(40):
+            if i % 4 == 0:
+                fn.flashnorm_rope_table_scaled(61, rot, base=10000.0 + 100 * i, out=cs)
+                between()
+            fn.flashnorm_rope(y, cs, pos, n_rope_heads=H - i % 2, layout=layout, backward=i % 3 == 2, out=y)
+            between()
+        return y
+
+    want = turn(x.clone(), torch.cuda.synchronize)
+    for _ in range(5):
+        assert torch.equal(turn(x.clone(), lambda: None), want)
