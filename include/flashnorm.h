@@ -357,8 +357,9 @@ FN_API fn_status flashnorm_int8_workspace_bytes(int64_t M, int64_t d, int64_t N,
  *   Rows whose target is ignore_index have a zero dx and take no part in dW*; a bad target gives its row a NaN dx, takes
  *   no part in dW* and is reported as above. lse is fp32, so the target's dl is known to 3.5e-6 g (|l| < 32): 0.35 % of
  *   itself where the target's probability is 0.999. r dl is rounded to bf16 once for the two products, but for the
- *   target's own entry, which stays fp32 (for dW* not where a class is frequent); sums are fp32. M == 0
- *   sets dWstar to zero.
+ *   target's own entry, which stays fp32. For dW* that entry is rounded too where, among 32 consecutive live rows, three or
+ *   more have targets within 32 neighbouring classes (V > 2048; frequent classes, or any three that lie close): such a row of
+ *   dW* has one rounding of 2^-8 at most per entry beside the output's. Sums are fp32. M == 0 sets dWstar to zero.
  * flashnorm_cross_entropy_workspace_bytes: the scratch a call (backward: 0 or 1) of this shape needs on the current
  *   device, written to *bytes; bounded by a piece of the vocabulary, not the whole. Caller-owned, 16-byte aligned,
  *   contents irrelevant before and after; calls whose kernels may overlap on the GPU must not share one. A smaller one

@@ -17,14 +17,16 @@
 // products (a batch half of prompt or padding costs half; what such rows hold cannot reach dW*). Then, in pieces of the
 // vocabulary, the logits are computed again and leave the chip as the factor both gradients share,
 //     P[m, n] = r[m] dl[m, n] in bf16,   dl[m, n] = g[m] (exp(l - lse) - [n = t]),
-// except for the target's own entry u[m] = r dl[m, t], which is taken from ce_row_dot and stays fp32 (P is 0 there; in blocks of 32 rows where three
-// targets or more lie within 32 classes of a large vocabulary P has it rounded, and u is the rest, which dW* then leaves out):
+// except for the target's own entry u[m] = r dl[m, t], which is taken from ce_row_dot and stays fp32 (P is 0 there; in blocks of
+// 32 live rows where three targets or more, equal or not, lie within 32 neighbouring classes of a large vocabulary, P has it
+// rounded, and u is the rest, which dW* then leaves out):
 //     dW*[n, :] = sum_m P[m, n] x[m, :] + sum_{m: t[m] = n} u[m] x[m, :]
 //     dx[m, :]  = sum_n P[m, n] W*[n, :] + u[m] W*[t, :] - x[m, :] (r[m]^2 / d) c[m],   c[m] = sum_n dl[m, n] l[m, n]
 // (the last term is the norm's own share: dr/dx = -r^3 x / d). The target's entry is most of a row's gradient and would
-// pass its rounding on to a whole row of dx and dW*: 0.0024 against 0.0017 relative, output rounding included. The other
-// entries' roundings, half a step of 2^-8 each, are independent and average out; tensor-core speed in both products
-// depends on them. Sums, c and the statistics are fp32.
+// pass its rounding on to a whole row of dx and dW*: 0.0024 against 0.0017 relative, output rounding included. That is what
+// the rows of dW* of such neighbouring targets get. The other entries are off by at most half a step, 2^-8 of themselves. Over many
+// rows or classes of like size that averages out; where one wrong class dominates a row, or few rows make up the batch, it
+// stays. Tensor-core speed in both products depends on it. Sums, c and the statistics are fp32.
 //
 // Measured at 2048 x 4096 x 32000 (each product 537 GFLOP): loss 335 us for the product, 12 around it; gradient, in two
 // pieces, packing 11, P 168 and both gradients' products 330 a piece, dx's last pass 21, together 1.04 ms for one call and
@@ -483,8 +485,10 @@ struct CeGradEpi {
       const int at = t0 - c0;
       const bool hit = row < t.M && at >= 0 && at < 32 && c0 + at < t.width;
       const unsigned hits = __ballot_sync(0xffffffffu, hit);
-      // `often` rows of the block or more: a frequent class, whose many entries' roundings average out. dW* takes them from P
-      // then, so that no warp of its epilogue has more than two rows in 32 to add by itself (2048 x 1024 x 32000 with a
+      // `often` rows of the block or more, of one frequent class or of several next to each other (ids in order of frequency,
+      // as vocabularies have them): dW* takes their entries from P, with one rounding each, so that no warp of its epilogue
+      // has more than two rows in 32 to add by itself. Counting only rows of one class and keeping the first two others of
+      // each block exact takes 420 us for 2048 x 1024 x 32000 with targets of frequency 1 / id, 340 so (2048 x 1024 x 32000 with a
       // tenth of the rows, or all, of one class: 341 and 318 us; 496 and 2323 if all are added there; 326 with none).
       const bool often = __popc(hits) >= e.often;
       if (lane == 0) e.live.hits[static_cast<size_t>((t.n0 + c0) >> 5) * e.live.ld_hits + (t.row0 >> 5)] = often ? 0u : hits;
@@ -521,7 +525,7 @@ struct CeGradEpi {
 // while the MMAs run it lists the live rows that have one of them (from the masks that P's epilogue left, 4 bytes per 32
 // live rows), lane k the k-th. They are added in their order, eight at a time: the lanes load the chunk's 32 columns of
 // u x (for the first eight one chunk ahead) and pass them through the staging buffer to the lane whose row it is. A warp
-// with more than 32 hits (a frequent token) lists the further ones again in every chunk.
+// with more than 32 hits lists the further ones again in every chunk.
 struct CeDwParams {
   CeLive live;
   const uint16_t* xc;  // [live rows][ldy]

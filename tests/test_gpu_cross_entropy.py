@@ -415,3 +415,35 @@ def test_shifted_labels_and_sliced_vectors(M):
     again = fn.flashnorm_linear_cross_entropy_backward(g1, x, W, labels, lse1, EPS)
     assert torch.equal(again[0], dx) and torch.equal(again[1], dW)
     fn.flashnorm_check_device_error()
+
+
+@pytest.mark.parametrize("what", ["neighbours", "equal rows", "crowd"])
+def test_neighbouring_targets(what):
+    """Targets that share a block of 32 rows and 32 classes: three different classes, each once; one class whose rows have the
+    same norm, g and logit, so that their entries round the same way; and 20 rows of six classes. The target's entry may be
+    rounded once, by 2^-8 of itself, and the output once: no element of dW* is further off than both, no row in norm
+    than 2^-7, and the rows of lone targets, held in fp32, than the output's rounding: 2^-8."""
+    M, d, V = 96, 136, 4096
+    x, W, t, g = _draw(M, d, V, seed=21)
+    t = torch.from_numpy(np.random.default_rng(2).permutation(np.arange(64, V, 32))[:M])  # one target in 32 classes
+    g = torch.full((M,), 0.37)
+    if what == "neighbours":
+        t[[3, 9, 30]] = torch.tensor([5, 17, 31])
+    elif what == "equal rows":
+        x[:40] = x[0]
+        t[:40] = 7
+    else:
+        t[40:60] = torch.arange(20) % 6
+    _, lse, _, _, ctx = _forward(x, W, t, EPS, -100)
+    dx, dW = fn.flashnorm_linear_cross_entropy_backward(g.cuda(), x.cuda(), W.cuda(), t.cuda(), lse.float().cuda(), EPS)
+    want_dx, want_dW, t_dx, t_dW = _backward(g, lse.float(), ctx)
+    _near(dx, want_dx, t_dx, "dx")
+    _near(dW, want_dW, t_dW, "dW")
+    off = (dW.double().cpu() - want_dW).norm(dim=1)
+    size, f32 = want_dW.norm(dim=1), t_dW[1].norm(dim=1)
+    rows = t.unique()
+    lone = rows[rows >= 64]
+    assert (off[rows] <= 2.0 ** -7 * size[rows] + f32[rows]).all()
+    # beside the target's entry a lone row has the others' entries, rounded too
+    rest = HB * ((ctx[2] * torch.exp(ctx[3] - lse[:, None]) * g.double()[:, None]).scatter(1, t[:, None], 0.0).T @ ctx[0].abs()).norm(dim=1)
+    assert (off[lone] <= HB * size[lone] + f32[lone] + rest[lone]).all()
