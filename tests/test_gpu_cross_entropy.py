@@ -447,3 +447,43 @@ def test_neighbouring_targets(what):
     # beside the target's entry a lone row has the others' entries, rounded too
     rest = HB * ((ctx[2] * torch.exp(ctx[3] - lse[:, None]) * g.double()[:, None]).scatter(1, t[:, None], 0.0).T @ ctx[0].abs()).norm(dim=1)
     assert (off[lone] <= HB * size[lone] + f32[lone] + rest[lone]).all()
+
+
+@pytest.mark.parametrize("M,d,V", [(1, 1032, 300), (16, 4096, 2000), (17, 2056, 20000), (24, 3000, 700), (31, 1088, 19500),
+                                   (32, 4096, 1000), (33, 4096, 1000), (32, 2048, 20100), (33, 2056, 20100)])
+def test_loss_of_few_rows_with_several_accumulations(M, d, V):
+    """More than 1024 k, so that a slab's sums are carried over several accumulations, the last one short; both sides of the
+    row count where the kernel changes; vocabularies of more than 128 rows per SM, so that CTAs take several slabs."""
+    x, W, t, g = _draw(M, d, V, seed=M + d)
+    loss, lse = fn.flashnorm_linear_cross_entropy(x.cuda(), W.cuda(), t.cuda(), EPS)
+    want, want_lse, tol, tol_lse, ctx = _forward(x, W, t, EPS, -100)
+    assert ((loss.double().cpu() - want).abs() <= tol).all()
+    assert ((lse.double().cpu() - want_lse).abs() <= tol_lse).all()
+    dx, dW = fn.flashnorm_linear_cross_entropy_backward(g.cuda(), x.cuda(), W.cuda(), t.cuda(), lse, EPS)
+    want_dx, want_dW, t_dx, t_dW = _backward(g, lse.cpu(), ctx)
+    _near(dx, want_dx, t_dx, "dx")
+    _near(dW, want_dW, t_dW, "dW")
+    fn.flashnorm_check_device_error()
+
+
+@pytest.mark.parametrize("M,d,V", [(8200, 64, 10000), (8200, 192, 10003)])
+def test_three_pieces_of_the_vocabulary(M, d, V):
+    """The second and third piece add to dx; operands of whole 64-column blocks. 64 bits on the GPU, in norm and row by row. A
+    row's gradient has the roundings of P and of the output, 2^-8 each at most."""
+    x, W, t, g = (v.cuda() for v in _draw(M, d, V, seed=13))
+    loss, lse = fn.flashnorm_linear_cross_entropy(x, W, t, EPS)
+    dx, dW = fn.flashnorm_linear_cross_entropy_backward(g, x, W, t, lse, EPS)
+    xd, Wd = x.double(), W.double()
+    r = 1 / torch.sqrt((xd * xd).mean(dim=1, keepdim=True) + EPS)
+    l = (xd * r) @ Wd.T
+    live = t != -100
+    at = t.clamp(min=0)[:, None]
+    dl = torch.exp(l - lse.double()[:, None]).scatter_add_(1, at, torch.full_like(at, -1, dtype=torch.float64))
+    dl *= torch.where(live, g.double(), 0.0)[:, None]
+    dn = dl @ Wd
+    want_dx = r * (dn - xd * r * (dn * xd * r).mean(dim=1, keepdim=True))
+    want_dW = dl.T @ (xd * r)
+    for got, want in ((dx, want_dx), (dW, want_dW)):
+        off, size = (got.double() - want).norm(dim=1), want.norm(dim=1)
+        assert off.norm() <= 2.0 ** -7 * size.norm() and (off <= 2.0 ** -6 * size + 1e-7 * size.max()).all()
+    fn.flashnorm_check_device_error()
