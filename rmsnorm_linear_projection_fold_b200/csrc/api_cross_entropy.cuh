@@ -70,7 +70,9 @@ int ce_mn_width(int64_t d) { return d > 128 ? 256 : 128; }
 // product cut into K ranges. With few rows the pass costs more than it saves (5 x 1080 x 1843: 9 us).
 constexpr int64_t kCeSmallVocab = 2048;
 
-// What an item of so many stages takes, in stages: at least its epilogue.
+// What an item of so many stages takes, in stages: at least its epilogue. With 6, 12 and 24 of them the gradient of 517 x 576 x
+// 50257 takes 133, 125 and 146 us, of 60 x 1024 x 50000 97, 102 and 130, of 128 x 4096 x 32000 229, 217 and 266, of 300 x 2048 x
+// 32000 195 to 220, 192 and 179.
 int64_t ce_item_cost(int64_t kb) { return std::max<int64_t>(kb, 12); }
 
 // K ranges of a product that shares a launch with another: few enough planes, many enough items that the longest share of
@@ -91,14 +93,18 @@ int ce_extra(const fn::PairGemmParams& p, const fn::PairGemmParams& q) {
   return static_cast<int>(std::max<int64_t>(1, ce_item_cost(p.num_kb / p.ksplit) / ce_item_cost(q.num_kb / q.ksplit)));
 }
 
-// Up to so many rows the loss streams W* past the tokens (cross_entropy_small.cuh). Call after call at 576 x 49152 with 23, 33
-// and 64 rows: 17.5, 20.7 and 27.3 us so (the tokens' tile is fetched with every stage), 22.4, 23.6 and 22.9 on CTA pairs.
+// Up to so many rows the loss streams W* past the tokens (cross_entropy_small.cuh). Call after call, so and on CTA pairs:
+//   576 x 49152    1 row 15.8 and 24.6 us, 16 rows 17.2 and 22.1, 32 rows 19.2 and 22.6 (64 rows: 27.3 and 22.9, the tokens' tile
+//                  being fetched with every stage)
+//   4096 x 32000   1 row 48.7 and 76.4, 16 rows 50.1 and 56.1, 32 rows 52.8 and 56.6
+//   1024 x 128256  1 row 47.8 and 73.2, 16 rows 49.2 and 71.2, 32 rows 52.2 and 67.4
 constexpr int kCeSmallRows = 32;
 constexpr int kCeFwdParts = fn::CeFwdEpi<false>::kParts;
 
 // P of a piece: at most so many bytes, unless that were fewer than kCePieceMin columns, between which dx's sums (8 bytes read
-// and written per element) would weigh too much. At 2048 x 4096 x 32000 (two pieces) the gradient takes 1.18 ms, 1.24 with
-// half the bytes, 1.16 with room for all of P.
+// and written per element) would weigh too much. With half the bytes, so, and with room for all of P the gradient takes 1.28,
+// 1.23 and 1.20 ms at 2048 x 4096 x 32000, 2.92, 2.66 and 2.56 at 4096 x 2048 x 65536 (512 MB), 0.89, 0.79 and 0.67 to 0.73 at
+// 4096 x 576 x 49152: memory against time.
 constexpr int64_t kCePieceBytes = int64_t{64} << 20, kCePieceMin = 4096;
 
 CePlan ce_plan(int64_t M, int64_t d, int64_t V, bool backward, int sms) {

@@ -25,9 +25,9 @@
 // which it adds in its own registers.
 //
 // Warps: 0 = TMA producer, 1 = MMA issuer (leader) and tensor memory, the others epilogue, Epi::kParts (2 or 4) per lane
-// quarter. Four hide an epilogue's latencies better and leave each thread 96 registers instead of 168: the loss needs little
-// else (23 rows x 576 x 49152: 23 us with four, 26 with two), P's epilogue spills with four (170 us against 165 at 2048 x
-// 4096 x 16000).
+// quarter. Four leave each thread 96 registers instead of 168. The loss has four; two take 1 to 8 % less at the rows it serves
+// (2048 x 576 x 49152: 82 against 86 to 89 us, 2048 x 4096 x 32000: 345 against 350, 64 x 4096 x 32000: 56.6 against 57.8).
+// The others have two: P's epilogue spills with four (170 us against 165 at 2048 x 4096 x 16000).
 //
 // What bounds it: the tensor pipe, 86 % of cycles busy at 2048 x 4096 x 16000 (the clock then falls to 1.55 GHz: 1.6 PFLOP/s
 // for one launch, 1.3 back to back under the power cap); the L2 at k of a few stages or narrow tiles. One warp issues loads
