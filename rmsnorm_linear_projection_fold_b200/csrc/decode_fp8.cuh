@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kD8Threads, 1)
       const int u = u0 + i, st = u / F::kUnits - g0, half = u % F::kUnits;
       const int s = st % STAGES, b = i % kD8ABufs;
       const uint32_t ph = static_cast<uint32_t>(st / STAGES) & 1u, bph = static_cast<uint32_t>(i / kD8ABufs) & 1u;
-      if (!mbar_wait(&full[s], ph, abort_flag) || !mbar_wait(&aempty[b], bph ^ 1u, abort_flag)) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[s], ph, abort_flag) && mbar_wait(&aempty[b], bph ^ 1u, abort_flag))) {
         ok = false;
         break;
       }
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kD8Threads, 1)
     ss += __shfl_xor_sync(0xffffffffu, ss, 1);
 
     float v[kD8Tok];
-    if (ok) ok = mbar_wait(acc_full, 0, abort_flag);
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(acc_full, 0, abort_flag));
     if (ok && u1 > u0) {
       tc_fence_after_sync();
       uint32_t r0[16], r1[16], r2[16], r3[16];

@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     bool ok = true;
     float ss = 0.f, sx = 0.f;
     for (int kb = kb0; kb < kb1; ++kb) {
-      if (!mbar_wait(&full[s], ph, abort_flag)) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[s], ph, abort_flag))) {
         ok = false;
         break;
       }
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 
     float v[kDecTok];
     const bool have_acc = ok && kb1 > kb0;
-    if (ok && have_acc) ok = mbar_wait(acc_full, 0, abort_flag);
+    if (ok && have_acc) ok = __all_sync(0xffffffffu, mbar_wait(acc_full, 0, abort_flag));
     if (have_acc && ok) {
       tc_fence_after_sync();
       uint32_t r0[16], r1[16], r2[16], r3[16];

@@ -348,12 +348,12 @@ __global__ void __launch_bounds__(gemm_threads(EPI, SCALE), 1)
     for (int t = t_begin; t < t_end; ++t) {
       const int mt = t / p.num_n_tiles;
       const int nt = t % p.num_n_tiles;
-      if (!mbar_wait(&acc_full[acc], acc_ph, abort_flag)) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[acc], acc_ph, abort_flag))) break;
       tc_fence_after_sync();
       float r = 1.0f;
       if (SCALE) {
         // The explicit join: the scale of this tile's rows must be ready too.
-        if (!mbar_wait(&ss_full[sb], sb_ph, abort_flag)) break;
+        if (!__all_sync(0xffffffffu, mbar_wait(&ss_full[sb], sb_ph, abort_flag))) break;
         r = rinv[sb * kBM + row_in_tile];
         mbar_arrive(&ss_empty[sb]);
         sb ^= 1;
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(gemm_threads(EPI, SCALE), 1)
         // second time on the earlier phase of `empty`. That phase would then complete without the MMA's
         // commit, the refill would overlap a load in flight, and a later full phase would never
         // collect its bytes.
-        if (!mbar_wait(&full[s], ph, abort_flag)) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[s], ph, abort_flag))) {
           ok = false;
           break;
         }
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(gemm_threads(EPI, SCALE), 1)
         r_row = 1.0f / sqrtf(ss / static_cast<float>(p.K) + p.eps);
         last_m = mt;
       }
-      if (!mbar_wait(&ss_empty[sb], sb_ph ^ 1u, abort_flag)) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(&ss_empty[sb], sb_ph ^ 1u, abort_flag))) break;
       rinv[sb * kBM + row_in_tile] = r_row;
       mbar_arrive(&ss_full[sb]);
       sb ^= 1;

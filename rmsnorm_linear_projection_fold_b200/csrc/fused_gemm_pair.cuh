@@ -291,11 +291,11 @@ __global__ void __launch_bounds__(gemm_threads(EPI, SCALE), 1)
     for (int i = 0; i < n_items; ++i) {
       int mt, n0t, width;
       tile_at(i, mt, n0t, width);
-      if (!mbar_wait_cluster(&acc_full[acc], acc_ph, abort_flag)) break;
+      if (!__all_sync(0xffffffffu, mbar_wait_cluster(&acc_full[acc], acc_ph, abort_flag))) break;
       tc_fence_after_sync();
       float r = 1.0f, km = 0.0f;
       if (SCALE) {
-        if (!mbar_wait(&ss_full[sb], sb_ph, abort_flag)) break;
+        if (!__all_sync(0xffffffffu, mbar_wait(&ss_full[sb], sb_ph, abort_flag))) break;
         r = rinv[sb * kBM + row_in_tile];
         if (LN) km = kmu[sb * kBM + row_in_tile];
         mbar_arrive(&ss_empty[sb]);
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(gemm_threads(EPI, SCALE), 1)
       for (int kb = 0; fresh && kb < num_kb; ++kb) {
         // Every use read here is waited for in order, so this warp is never more than one xfull phase
         // behind and the parity wait is unambiguous.
-        if (!mbar_wait_cluster(&xfull[s], (x_ph >> s) & 1u, abort_flag)) {
+        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&xfull[s], (x_ph >> s) & 1u, abort_flag))) {
           ok = false;
           break;
         }
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(gemm_threads(EPI, SCALE), 1)
         }
         last_m = mt;
       }
-      if (!mbar_wait(&ss_empty[sb], sb_ph ^ 1u, abort_flag)) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(&ss_empty[sb], sb_ph ^ 1u, abort_flag))) break;
       rinv[sb * kBM + row_in_tile] = r_row;
       if (LN) kmu[sb * kBM + row_in_tile] = km_row;
       mbar_arrive(&ss_full[sb]);

@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kPpThreads, 1)
   const int nchunks = w / 16;
   bool ok = true;
   if (epi) {
-    ok = mbar_wait_cluster(acc_full, 0, abort_flag);
+    ok = __all_sync(0xffffffffu, mbar_wait_cluster(acc_full, 0, abort_flag));
     if (ok) tc_fence_after_sync();
   }
   // (1) every CTA's contraction is complete, so every CTA's stage buffers are idle

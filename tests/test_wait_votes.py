@@ -31,7 +31,7 @@ def _unvoted(code):
             blocks.pop()
         elif m.group() != ";":
             head = " ".join(blocks) + code[last:m.start()]
-            if not re.search(r"(lane|threadIdx\.x) == 0\b", head) and not code[:m.start()].endswith(VOTE):
+            if not re.search(r"(lane|threadIdx\.x) == 0\b", head) and not re.search(re.escape(VOTE) + r"([^;{}]*&& )?$", code[last:m.start()]):
                 found.append(code[:m.start()].count("\n") + 1)
             continue
         last = m.end()
@@ -41,6 +41,8 @@ def _unvoted(code):
 def test_the_reader_sees_an_unvoted_wait():
     assert _unvoted("void f() { if (lane == 0) { mbar_wait(a, 0, f); } }") == []
     assert _unvoted("void f() { bool ok = " + VOTE + "mbar_wait(a, 0, f)); }") == []
+    assert _unvoted("void f() { bool ok = " + VOTE + "mbar_wait(a, 0, f) && mbar_wait(b, 0, f)); }") == []
+    assert _unvoted("void f() { bool ok = " + VOTE + "mbar_wait(a, 0, f)) || mbar_wait(b, 0, f); }") == [1]
     assert _unvoted("void f() {\n if (!mbar_wait_cluster(a, 0, f)) return; }") == [2]
 
 
@@ -67,3 +69,10 @@ def test_a_loss_whose_product_gave_up_is_not_joined_from_what_lies_in_the_worksp
     assert re.search(r"grid_dep_wait\(\);.* gave_up = __ldcg\(failed\);.*ce_join_row<.*if \(gave_up != 0u[^;]*\) loss\[row\] = lse\[row\] = "
                      r"__int_as_float\(0x7fc00000\)", join, re.S)
     assert "launch_rstd(x, rstd, p.failed," in host
+
+
+@pytest.mark.parametrize("name", ["decode_tc.cuh", "decode_fp8.cuh", "fused_gemm.cuh", "fused_gemm_pair.cuh", "postnorm_pair.cuh",
+                                  "postnorm_split.cuh"])
+def test_waits_of_whole_warps_are_voted_on_in_the_projections(name):
+    code = _code(name)
+    assert "mbar_wait" in code and _unvoted(code) == []
