@@ -360,6 +360,9 @@ FN_API fn_status flashnorm_int8_workspace_bytes(int64_t M, int64_t d, int64_t N,
  *   target's own entry, which stays fp32. For dW* that entry is rounded too where, among 32 consecutive live rows, three or
  *   more have targets within 32 neighbouring classes (V > 2048; frequent classes, or any three that lie close): such a row of
  *   dW* has one rounding of 2^-8 at most per entry beside the output's. Sums are fp32. M == 0 sets dWstar to zero.
+ *   dWstar is the gradient of the folded matrix. Of W [d, V] and the gain that were folded into it,
+ *     dW[k][n] = gain[k] dW*[n][k],   dgain[k] = sum_n W[k][n] dW*[n][k]  (the fold's rounding passed over),
+ *   which the caller forms.
  * flashnorm_cross_entropy_workspace_bytes: the scratch a call (backward: 0 or 1) of this shape needs on the current
  *   device, written to *bytes; bounded by a piece of the vocabulary, not the whole. Caller-owned, 16-byte aligned,
  *   contents irrelevant before and after; calls whose kernels may overlap on the GPU must not share one. A smaller one
@@ -418,7 +421,8 @@ FN_API fn_status flashnorm_rope(const void* x, const void* rope_cs, const void* 
  *   NTK     base replaced by base * factor^(rot_dim / (rot_dim - 2))
  *   YARN    theta_i (k_i + (1 - k_i) / factor), k_i = clamp((t_i - alpha) / (beta - alpha), 0, 1),
  *           t_i = original_max_pos theta_i / (2 pi) ("YaRN: Efficient Context Window Extension of Large Language
- *           Models", NTK-by-parts)
+ *           Models", NTK-by-parts: the blend is linear in the number of turns. Code that blends linearly over the pair
+ *           index i between two rounded indices has other angles between them)
  * cos and sin are both multiplied by attention_factor (1 for none). Double precision, rounded once to fp32.
  */
 FN_API fn_status flashnorm_rope_table_scaled(void* rope_cs, int64_t max_pos, int64_t rot_dim, double base, int scaling,

@@ -708,7 +708,9 @@ def flashnorm_rope_table_scaled(max_pos: int, rot_dim: int, base: float = 10000.
 
     scaling: "none"; "linear" (positions divided by factor); "ntk" (base times factor^(rot_dim / (rot_dim - 2)));
     "yarn" (by parts: pairs that turn at least beta times within original_max_pos keep their angle, those that turn
-    at most alpha times are divided by factor, a linear blend between). attention_factor multiplies cos and sin;
+    at most alpha times are divided by factor, a blend between that is linear in the number of turns, as in the paper;
+    a checkpoint whose code blends linearly over the pair index between two rounded indices has other angles there).
+    attention_factor multiplies cos and sin;
     the default is 0.1 ln(factor) + 1 for "yarn" and 1 otherwise."""
     if scaling not in ROPE_SCALINGS:
         raise ValueError('scaling must be "none", "linear", "ntk" or "yarn"')
@@ -866,7 +868,8 @@ def flashnorm_linear_cross_entropy(x: torch.Tensor, Wstar: torch.Tensor, targets
                                    ignore_index: int = -100, workspace="auto"):
     """(loss, lse), fp32 [M]: softmax cross entropy of the logits r x . W* (final RMSNorm, then the vocabulary head),
     which are never stored. x [M, d] bf16, W* [V, d] bf16 from fold_weights, targets int64 [M]; a row whose target is
-    ignore_index has loss 0. workspace: "auto", or a uint8 CUDA tensor of at least
+    ignore_index has loss 0. Like every call of this package it takes no part in autograd: the results are detached, and
+    the gradient is the call below. workspace: "auto", or a uint8 CUDA tensor of at least
     flashnorm_cross_entropy_workspace_bytes(M, d, V) bytes."""
     M, d, V = _ce_call(x, Wstar, targets)
     loss = x.new_empty(M, dtype=torch.float32)
@@ -883,7 +886,8 @@ def flashnorm_linear_cross_entropy_backward(grad_loss: torch.Tensor, x: torch.Te
                                             targets: torch.Tensor, lse: torch.Tensor, eps: float,
                                             ignore_index: int = -100, workspace="auto"):
     """(dx [M, d], dWstar [V, d]), bf16: the gradient of flashnorm_linear_cross_entropy's losses weighted with grad_loss
-    (fp32 [M]); lse is the forward's. The logits are computed again in pieces of the vocabulary. workspace: "auto", or
+    (fp32 [M]); lse is the forward's. dWstar is that of the folded matrix: with W* = fold_weights(W, gain),
+    dW = gain[:, None] * dWstar.T and dgain = (W * dWstar.T).sum(1). The logits are computed again in pieces of the vocabulary. workspace: "auto", or
     a uint8 CUDA tensor of at least flashnorm_cross_entropy_workspace_bytes(M, d, V, backward=True) bytes."""
     M, d, V = _ce_call(x, Wstar, targets)
     _need(grad_loss, "grad_loss", torch.float32, dim=1)
