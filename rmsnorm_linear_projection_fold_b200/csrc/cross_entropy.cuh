@@ -28,8 +28,8 @@
 // rows or classes of like size that averages out; where one wrong class dominates a row, or few rows make up the batch, it
 // stays. Tensor-core speed in both products depends on it. Sums, c and the statistics are fp32.
 //
-// Measured at 2048 x 4096 x 32000 (each product 537 GFLOP): loss 335 us for the product, 12 around it; gradient, in two
-// pieces, packing 11, P 168 and both gradients' products 330 a piece, dx's last pass 21, together 1.04 ms for one call and
+// Measured at 2048 x 4096 x 32000 (each product 537 GFLOP): loss 326 us for the product, 7 and 12 around it; gradient, in two
+// pieces, packing 11, P 166 and both gradients' products 338 a piece, dx's last pass 20, together 1.04 ms for one call and
 // 1.25 back to back under the power cap (cuBLAS's rate there is 1.42 PFLOP/s: 1.13 ms for the products alone).
 // At 517 x 576 x 50257 (a tile of dW* has 8 stages of k): P 34, products 68 us, bound by the L2 and the epilogues.
 #pragma once
