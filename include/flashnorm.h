@@ -21,7 +21,8 @@
  *     allocates, frees or keeps them. Pointers must be 16-byte aligned, unless an entry point asks for less.
  *   - Element types: activations, weights, gains and the unfused intermediate are bf16 (stored as
  *     uint16 bit patterns); outputs are bf16 or fp32 as `out_dtype` says. All arithmetic is fp32
- *     with one round-to-nearest-even conversion per bf16 result.
+ *     with one round-to-nearest-even conversion per bf16 result. That includes a row's sum of squares: where it passes
+ *     3.4e38 (elements near 1e19 / sqrt(d) and above), 1/rms is 0.
  *   - Layouts are row-major. x is [M, d]; y is [M, N] (linear, post-norm) or [M, F] (GLU).
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default stream). Every call only
  *     enqueues work on it and returns; nothing synchronises except flashnorm_check_device_error.
