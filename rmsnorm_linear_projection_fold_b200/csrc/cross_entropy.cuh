@@ -108,7 +108,8 @@ __device__ __forceinline__ float ce_row_dot(const uint16_t* x, const uint16_t* w
 struct CeFwdParams {
   const float* rstd;
   const long long* targets;
-  float2* part;  // [M][kParts column tiles]: running maximum (of log2 e times the logits) and sum of 2^(. - max), the target left out
+  // [M][kParts column tiles]: running maximum (of log2 e times the logits) and sum of 2^(. - max), the target left out
+  float2* part;
 };
 
 // A thread's columns of a tile are up to kChunks chunks of 32, shared out among the quarter's warps. HELD: the tile takes
@@ -300,16 +301,16 @@ struct CeLive {
 constexpr int kCeIgnored = -1, kCeBad = -2;  // in place of a row's rank among the live ones
 
 // Packs the live rows in order: xc[rank] = x[m], rows[rank], the target's entry u[rank] and its share ct[rank] of c / r,
-// rank_of[m], and their number. Rows up to the next multiple of
-// 64 are zeroed: dW*'s product runs over whole stages of 64 rows. A block serves rows_per_block rows, a warp an eighth of
-// them in order; each counts the live rows before its own, from the targets.
+// rank_of[m], and their number. Rows up to the next multiple of 64 are zeroed: dW*'s product runs over whole stages of 64
+// rows. A block serves rows_per_block rows, a warp an eighth of them in order; each counts the live rows before its own, from
+// the targets. 2048 x 4096: 11.4 us for 33 MB from HBM, latency: one row a warp.
 __global__ void __launch_bounds__(256, 2) k_ce_pack(const uint16_t* __restrict__ x, const long long* __restrict__ targets,
-                                                 const float* __restrict__ lse, const float* __restrict__ g,
-                                                 const uint16_t* __restrict__ W, uint16_t* __restrict__ xc,
-                                                 CeRow* __restrict__ rows, int* __restrict__ target, float* __restrict__ u,
-                                                 float* __restrict__ ct, int* __restrict__ rank_of,
-                                                 int* __restrict__ n_live, int M, int K, int V,
-                                                 int rows_per_block, float eps, long long ignore) {
+                                                    const float* __restrict__ lse, const float* __restrict__ g,
+                                                    const uint16_t* __restrict__ W, uint16_t* __restrict__ xc,
+                                                    CeRow* __restrict__ rows, int* __restrict__ target,
+                                                    float* __restrict__ u, float* __restrict__ ct,
+                                                    int* __restrict__ rank_of, int* __restrict__ n_live, int M, int K,
+                                                    int V, int rows_per_block, float eps, long long ignore) {
   grid_dep_wait();
   grid_dep_launch();
   __shared__ int counts[8];
